@@ -1,7 +1,8 @@
 """Build libmoe_ep.so and libmoe_streams.so (HIP, gfx950) in-tree with hipcc.
 
 Each .hip source is compiled to an object in parallel, then linked into
-``combine_lds_atomic_amd/libmoe_ep.so`` (dispatch / combine, include/moe_ep.h)
+``combine_lds_atomic_amd/libmoe_ep.so`` (dispatch / combine and the expert
+layer, include/moe_ep.h)
 and ``combine_lds_atomic_amd/libmoe_streams.so`` (the benchmark's plain
 streams, include/moe_streams.h).  Usage: ``python
 combine_lds_atomic_amd/build.py`` (or ``__graft_entry__.build()``); run it by
@@ -24,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_ep.so")
 STREAMS_LIB = os.path.join(PKG, "libmoe_streams.so")
-SOURCES = ["abi.hip", "layout.hip", "dispatch.hip", "combine.hip"]
+SOURCES = ["abi.hip", "layout.hip", "dispatch.hip", "combine.hip", "norm.hip", "gemm.hip", "layer.hip"]
 STREAMS_SOURCES = ["streams.hip"]
 ARCH = "gfx950"
 

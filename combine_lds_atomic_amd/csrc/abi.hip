@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/moe_ep.h: argument checks,
 // workspace carving, grid sizing and launches on the caller's stream.
+#include <cmath>
 #include <mutex>
 
 #include "moe_internal.h"
@@ -182,6 +183,28 @@ int direct_args(const Dims& D, const uint16_t* tokens, const int32_t* topk_idx, 
   if (!aligned(topk_idx, 4) || !aligned(send_pos, 4) || !aligned(row_src, 4)) return MOE_EALIGN;
   if (tokens && (!aligned(tokens, 16) || !aligned(x_q, 16) || !aligned(x_s, 4))) return MOE_EALIGN;
   return MOE_OK;
+}
+
+// Host checks that the grouped products share: K input features, `out`
+// output features in steps of `step`; a_out is the 16-byte aligned output.
+int gemm_args(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q, const float* w_s,
+              const int32_t* exp_off, int32_t K, int32_t out, int32_t step, const void* a_out) {
+  if (K < kScaleBlock || K > kMaxH || K % kScaleBlock) return MOE_EINVAL;
+  if (out < step || out > kMaxH || out % step) return MOE_EINVAL;
+  if (D.T == 0) return MOE_OK;   // no rows: empty arrays may be NULL
+  if (!x_q || !x_s || !w_q || !w_s || !exp_off || !a_out) return MOE_ENULL;
+  if (!aligned(x_q, 16) || !aligned(w_q, 16) || !aligned(x_s, 4) || !aligned(w_s, 4) || !aligned(exp_off, 4) ||
+      !aligned(a_out, 16))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+// Host checks of the few-token layer's shape.
+int layer_dims(const moe_shape* shape, int32_t I, Dims* D) {
+  const int rc = make_dims(shape, D);
+  if (rc) return rc;
+  if (I < kScaleBlock || I > kMaxH || I % kScaleBlock) return MOE_EINVAL;
+  return (int64_t)D->N * D->T > kLayerMaxTokens ? MOE_EINVAL : MOE_OK;
 }
 
 }  // namespace
@@ -411,6 +434,68 @@ int moe_combine_recv_partial(const moe_shape* shape, const uint16_t* comb, const
   if (!aligned(comb, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) || !aligned(send_pos, 4)) return MOE_EALIGN;
   return launch_comb_recv_partial(D, W_of(D, const_cast<void*>(ws)), comb, topk_idx, send_pos, out, device_cus(),
                                   as_stream(stream));
+}
+
+int moe_rmsnorm_quant(const moe_shape* shape, const uint16_t* x, const uint16_t* residual, const uint16_t* gamma,
+                      float eps, uint16_t* res_out, uint16_t* y, uint8_t* y_q, float* y_s, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_EINVAL;
+  if (D.T == 0) return MOE_OK;
+  if (!x || !gamma || (!y && !y_q) || !y_q != !y_s) return MOE_ENULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(res_out, 16) || !aligned(y, 16) ||
+      !aligned(y_q, 16) || !aligned(y_s, 4))
+    return MOE_EALIGN;
+  return launch_rmsnorm_quant(D, x, residual, gamma, eps, res_out, y, y_q, y_s, as_stream(stream));
+}
+
+int moe_grouped_gemm(const moe_shape* shape, const uint8_t* x_q, const float* x_s, const uint8_t* w_q,
+                     const float* w_s, const int32_t* exp_off, int32_t K, int32_t F, uint16_t* y, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  rc = gemm_args(D, x_q, x_s, w_q, w_s, exp_off, K, F, 16, y);
+  if (rc || D.T == 0) return rc;
+  return launch_grouped_gemm(D, x_q, x_s, w_q, w_s, exp_off, K, F, y, device_cus(), as_stream(stream));
+}
+
+int moe_grouped_gemm_swiglu(const moe_shape* shape, const uint8_t* x_q, const float* x_s, const uint8_t* w13_q,
+                            const float* w13_s, const int32_t* exp_off, int32_t K, int32_t I, uint8_t* a_q,
+                            float* a_s, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  rc = gemm_args(D, x_q, x_s, w13_q, w13_s, exp_off, K, I, kScaleBlock, a_q);
+  if (rc || D.T == 0) return rc;
+  if (!a_s) return MOE_ENULL;
+  if (!aligned(a_s, 4)) return MOE_EALIGN;
+  return launch_grouped_gemm_swiglu(D, x_q, x_s, w13_q, w13_s, exp_off, K, I, a_q, a_s, device_cus(),
+                                    as_stream(stream));
+}
+
+int64_t moe_layer_ll_workspace_bytes(const moe_shape* shape, int32_t I) {
+  Dims D;
+  const int rc = layer_dims(shape, I, &D);
+  if (rc) return rc;
+  return (int64_t)up((size_t)D.N * D.TK * I * sizeof(uint32_t) + kAlign);
+}
+
+int moe_layer_ll(const moe_shape* shape, const uint16_t* tokens, const int32_t* topk_idx, const float* topk_w,
+                 const uint8_t* w13_q, const float* w13_s, const uint8_t* w2_q, const float* w2_s, int32_t I,
+                 uint16_t* out, uint32_t* flags, void* ws, void* stream) {
+  Dims D;
+  int rc = layer_dims(shape, I, &D);
+  if (rc) return rc;
+  if (!flags) return MOE_ENULL;
+  if (!aligned(flags, 4)) return MOE_EALIGN;
+  if (D.T == 0) return launch_fill_u32(flags, 0u, 1, as_stream(stream));   // empty arrays may be NULL
+  if (!tokens || !topk_idx || !topk_w || !w13_q || !w13_s || !w2_q || !w2_s || !out || !ws) return MOE_ENULL;
+  if (!aligned(tokens, 16) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(w13_q, 16) ||
+      !aligned(w13_s, 4) || !aligned(w2_q, 16) || !aligned(w2_s, 4) || !aligned(out, 16) || !aligned(ws, kAlign))
+    return MOE_EALIGN;
+  return launch_layer_ll(D, tokens, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, I, out, flags, ws,
+                         as_stream(stream));
 }
 
 int moe_status(void* ws, void* stream, uint32_t* flags) {

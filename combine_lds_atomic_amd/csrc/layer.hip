@@ -1,0 +1,395 @@
+// The experts' part of a whole MoE layer for a few tokens, in two kernels:
+//
+//   out[t] = bf16( sum_j w[t][j] * W2[e] ( silu(Wg[e] x_t) * (Wu[e] x_t) ) ),  e = topk_idx[t][j]
+//
+// with e4m3 weights and a scale for each 128x128 block, and the tokens in
+// bf16.  Every weight that some token needs is read once; at these sizes
+// nothing else counts.  e4m3 converts to bf16 exactly, so the products run on
+// bf16 matrix instructions and nothing but the output is rounded to 8 or 16
+// bits: the activation between the two products is held as the sum of two
+// bf16 (16 significand bits), multiplied one after the other.
+#include "moe_internal.h"
+#include "quant_dev.h"
+
+namespace moe {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+struct LayerArgs {
+  const uint16_t* x;
+  const int* idx;
+  const float* w;
+  const uint8_t* w13_q;
+  const float* w13_s;
+  const uint8_t* w2_q;
+  const float* w2_s;
+  uint16_t* out;
+  uint32_t* flags;
+  uint16_t* a_hi;   // [slots][I]: the weighted activation's upper bf16
+  uint16_t* a_lo;   // [slots][I]: what is left of it
+  int tokens, slots, k, E, H, I;
+};
+
+constexpr int kLayerUpWaves = 4;
+constexpr int kLayerDownWaves = 8;
+constexpr int kLayerMaxSlots = kLayerMaxTokens * kMaxK;
+static_assert(kLayerMaxTokens <= kWave, "a lane for each token");
+
+// The call's distinct experts, ascending, and every slot's expert (-1 for an
+// id outside [0, E)).
+struct LayerRoutes {
+  int16_t id[kLayerMaxSlots];
+  int16_t experts[kMaxE];
+  uint32_t mask[kMaxE / 32];
+  int count;
+};
+
+// Fills R; returns whether this thread saw a bad id.  Ends with a barrier.
+__device__ __forceinline__ bool layer_routes(const LayerArgs& A, LayerRoutes& R) {
+  bool bad = false;
+  if (threadIdx.x < kMaxE / 32) R.mask[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int s = threadIdx.x; s < A.slots; s += blockDim.x) {
+    int e = A.idx[s];
+    if (e < 0 || e >= A.E) {
+      bad = true;
+      e = -1;
+    } else {
+      atomicOr(&R.mask[e >> 5], 1u << (e & 31));
+    }
+    R.id[s] = (int16_t)e;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) {
+    const uint32_t m = R.mask[e >> 5];
+    int before = __popc(m & ((1u << (e & 31)) - 1u));
+    for (int i = 0; i < (e >> 5); ++i) before += __popc(R.mask[i]);
+    if (m >> (e & 31) & 1u) R.experts[before] = (int16_t)e;
+    if (e == kMaxE - 1) R.count = before + (int)(m >> 31);
+  }
+  __syncthreads();
+  return bad;
+}
+
+// The tokens that chose expert e, ascending: lane c < n has the c-th one's
+// number, its weight (summed over its slots of e, in slot order) and the
+// first of these slots, which names its row of the activation.
+struct LayerMembers {
+  int n, token, slot;
+  float weight;
+};
+
+__device__ __forceinline__ LayerMembers layer_members(const LayerArgs& A, const LayerRoutes& R, int e) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int slot = -1;
+  float w = 0.0f;
+  if (lane < A.tokens)
+    for (int j = A.k - 1; j >= 0; --j)
+      if (R.id[lane * A.k + j] == e) slot = lane * A.k + j;
+  if (slot >= 0)
+    for (int j = slot - lane * A.k; j < A.k; ++j)
+      if (R.id[lane * A.k + j] == e) w += A.w[lane * A.k + j];
+  const unsigned long long in = __ballot(slot >= 0), below = (1ull << lane) - 1ull;
+  LayerMembers M;
+  M.n = __popcll(in);
+  const int to = (slot >= 0 ? __popcll(in & below) : M.n + __popcll(~in & below)) * 4;
+  M.token = __builtin_amdgcn_ds_permute(to, lane);
+  M.slot = __builtin_amdgcn_ds_permute(to, slot);
+  M.weight = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(w)));
+  return M;
+}
+
+__device__ __forceinline__ v8bf as_bf(const v4u& a) { return __builtin_bit_cast(v8bf, a); }
+__device__ __forceinline__ v4u ld16_cached(const void* p) { return *static_cast<const v4u*>(p); }
+
+// One 128-column block of a 16-row weight tile: lane l holds, of row l % 16,
+// columns h*64 + (l/16)*16 .. + 15 for h = 0, 1.  Product (h, s) takes the
+// 8 columns from h*64 + (l/16)*16 + s*8 of both operands: a permutation of
+// the block's columns, the same on both sides.
+struct WBlock {
+  v4u q[2];
+};
+__device__ __forceinline__ WBlock load_w(const uint8_t* p) {
+  WBlock b;
+  b.q[0] = ld16(reinterpret_cast<const v4u*>(p));
+  b.q[1] = ld16(reinterpret_cast<const v4u*>(p + 64));
+  return b;
+}
+// The same block of one token's bf16 row.
+struct XBlock {
+  v4u v[4];
+};
+__device__ __forceinline__ XBlock load_x(const uint16_t* p) {
+  XBlock b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b.v[i] = ld16_cached(p + (i >> 1) * 64 + (i & 1) * 8);
+  return b;
+}
+__device__ __forceinline__ v8bf w_part(const WBlock& b, int i) {
+  return widen8(b.q[i >> 1][(i & 1) * 2], b.q[i >> 1][(i & 1) * 2 + 1]);
+}
+
+// Gate and up rows [i0, i0 + 16) of expert e times the NT*16 members from c0
+// on; wave w takes blocks w, w + 4, ...; then the waves' sums are joined in
+// LDS.
+template <int NT>
+__device__ __forceinline__ void layer_up_tile(const LayerArgs& A, const LayerMembers& M, int e, int i0, int c0,
+                                              float (*red)[2][NT * 16][17]) {
+  constexpr int kXBufs = NT == 1 ? 2 : 1;   // with more columns the tokens' blocks are loaded when needed
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int KB = A.H / kScaleBlock, IB = A.I / kScaleBlock;
+  const uint8_t* wg = A.w13_q + ((int64_t)e * 2 * A.I + i0 + (lane & 15)) * A.H + (lane >> 4) * 16;
+  const uint8_t* wu = wg + (int64_t)A.I * A.H;
+  const float* sg = A.w13_s + ((int64_t)e * 2 * IB + i0 / kScaleBlock) * KB;
+  const float* su = sg + (int64_t)IB * KB;
+  const uint16_t* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int c = c0 + n * 16 + (lane & 15);
+    xp[n] = A.x + (int64_t)__shfl(M.token, c < M.n ? c : 0) * A.H + (lane >> 4) * 16;
+  }
+  v4f ag[NT], au[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) ag[n] = au[n] = v4f{0, 0, 0, 0};
+  WBlock g[2], u[2];
+  XBlock x[kXBufs][NT];
+  auto fetch_x = [&](int slot, int kb) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[slot][n] = load_x(xp[n] + kb * kScaleBlock);
+  };
+  auto fetch = [&](int slot, int kb) {
+    if (kb < KB) {
+      g[slot] = load_w(wg + kb * kScaleBlock);
+      u[slot] = load_w(wu + kb * kScaleBlock);
+      if (kXBufs == 2) fetch_x(slot % kXBufs, kb);
+    }
+  };
+  auto step = [&](int slot, int kb) {
+    const float s0 = sg[kb], s1 = su[kb];
+    if (kXBufs == 1) fetch_x(0, kb);
+    const XBlock* xs = x[slot % kXBufs];
+    v4f pg[NT], pu[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) pg[n] = pu[n] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v8bf a = w_part(g[slot], i), b = w_part(u[slot], i);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        pg[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(xs[n].v[i]), pg[n], 0, 0, 0);
+        pu[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, as_bf(xs[n].v[i]), pu[n], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ag[n][i] = __builtin_fmaf(pg[n][i], s0, ag[n][i]);
+        au[n][i] = __builtin_fmaf(pu[n][i], s1, au[n][i]);
+      }
+  };
+  // Two blocks of weights on their way while one is multiplied.
+  fetch(0, wave);
+  fetch(1, wave + kLayerUpWaves);
+  for (int kb = wave; kb < KB; kb += 2 * kLayerUpWaves) {
+    step(0, kb);
+    fetch(0, kb + 2 * kLayerUpWaves);
+    if (kb + kLayerUpWaves < KB) {
+      step(1, kb + kLayerUpWaves);
+      fetch(1, kb + 3 * kLayerUpWaves);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      red[wave][0][n * 16 + (lane & 15)][(lane >> 4) * 4 + i] = ag[n][i];
+      red[wave][1][n * 16 + (lane & 15)][(lane >> 4) * 4 + i] = au[n][i];
+    }
+  __syncthreads();
+  const int r = threadIdx.x & 15;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {   // 256 threads: 16 members x 16 rows
+    const int cl = n * 16 + threadIdx.x / 16, c = c0 + cl;
+    float gt = 0.0f, up = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kLayerUpWaves; ++v) {
+      gt += red[v][0][cl][r];
+      up += red[v][1][cl][r];
+    }
+    const int slot = __shfl(M.slot, c);
+    const float w = __shfl(M.weight, c);
+    if (c < M.n) {
+      const float v = gt / (1.0f + __expf(-gt)) * up * w;
+      const uint32_t hi = f32_to_bf16_rne(v);
+      const float left = v - __uint_as_float(hi << 16);
+      const int64_t at = (int64_t)slot * A.I + i0 + r;
+      A.a_hi[at] = (uint16_t)hi;
+      // Infinity and NaN are in the upper part alone.
+      A.a_lo[at] = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0 : (uint16_t)f32_to_bf16_rne(left);
+    }
+  }
+}
+
+template <int NT>
+__global__ __launch_bounds__(kLayerUpWaves* kWave) void k_layer_up(LayerArgs A) {
+  __shared__ LayerRoutes R;
+  __shared__ float red[kLayerUpWaves][2][NT * 16][17];
+  const bool bad = layer_routes(A, R);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *A.flags = any ? MOE_FLAG_BADID : 0u;
+  }
+  if ((int)blockIdx.y >= R.count) return;
+  const int e = __builtin_amdgcn_readfirstlane(R.experts[blockIdx.y]);
+  const LayerMembers M = layer_members(A, R, e);
+  for (int c0 = 0; c0 < M.n; c0 += NT * 16) {
+    if (c0) __syncthreads();   // red is read until here
+    layer_up_tile<NT>(A, M, e, blockIdx.x * 16, c0, red);
+  }
+}
+
+// Output rows [h0, h0 + 16*RT) of expert e over blocks [k0, k1), of the NT*16
+// members from c0 on, added to the wave's own sums acc[token][16*RT].
+template <int RT, int NT>
+__device__ __forceinline__ void layer_down_part(const LayerArgs& A, const LayerMembers& M, int e, int h0, int k0,
+                                                int k1, int c0, float* acc) {
+  constexpr int kXBufs = NT == 1 ? 2 : 1;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int IB = A.I / kScaleBlock, HB = A.H / kScaleBlock;
+  const uint8_t* wp[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    wp[r] = A.w2_q + ((int64_t)e * A.H + h0 + r * 16 + (lane & 15)) * A.I + (lane >> 4) * 16;
+  const float* sp = A.w2_s + ((int64_t)e * HB + h0 / kScaleBlock) * IB;
+  int64_t ap[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int c = c0 + n * 16 + (lane & 15);
+    ap[n] = (int64_t)__shfl(M.slot, c < M.n ? c : 0) * A.I + (lane >> 4) * 16;
+  }
+  v4f o[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[r][n] = v4f{0, 0, 0, 0};
+  WBlock w[2][RT];
+  XBlock hi[kXBufs], lo[kXBufs];
+  auto fetch = [&](int slot, int kb) {
+    if (kb < k1) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) w[slot][r] = load_w(wp[r] + kb * kScaleBlock);
+      if (kXBufs == 2) {
+        hi[slot % kXBufs] = load_x(A.a_hi + ap[0] + kb * kScaleBlock);
+        lo[slot % kXBufs] = load_x(A.a_lo + ap[0] + kb * kScaleBlock);
+      }
+    }
+  };
+  auto step = [&](int slot, int kb) {
+    const float s = sp[kb];
+    v4f p[RT][NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (kXBufs == 1) {
+        hi[0] = load_x(A.a_hi + ap[n] + kb * kScaleBlock);
+        lo[0] = load_x(A.a_lo + ap[n] + kb * kScaleBlock);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        p[r][n] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const v8bf a = w_part(w[slot][r], i);
+          p[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(hi[slot % kXBufs].v[i]), p[r][n], 0, 0, 0);
+          p[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf(lo[slot % kXBufs].v[i]), p[r][n], 0, 0, 0);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[r][n][i] = __builtin_fmaf(p[r][n][i], s, o[r][n][i]);
+  };
+  fetch(0, k0);
+  fetch(1, k0 + 1);
+  for (int kb = k0; kb < k1; kb += 2) {
+    step(0, kb);
+    fetch(0, kb + 2);
+    if (kb + 1 < k1) {
+      step(1, kb + 1);
+      fetch(1, kb + 3);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int c = c0 + n * 16 + (lane & 15);
+    const int token = __shfl(M.token, c);
+    if (c < M.n)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        v4f* p = reinterpret_cast<v4f*>(acc + (token * RT + r) * 16 + (lane >> 4) * 4);
+        *p = *p + o[r][n];
+      }
+  }
+}
+
+// Workgroup b forms output rows [b*16*RT, ...) of every token.  The blocks of
+// all distinct experts, expert after expert, are split evenly over the waves;
+// each wave adds its products into LDS sums of its own, which are joined in
+// wave order, so the result does not depend on timing.
+template <int RT, int NT>
+__global__ __launch_bounds__(kLayerDownWaves* kWave) void k_layer_down(LayerArgs A) {
+  __shared__ LayerRoutes R;
+  __shared__ __align__(16) float sums[kLayerDownWaves][kLayerMaxTokens * RT * 16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+  for (int i = lane; i < A.tokens * RT * 16; i += kWave) sums[wave][i] = 0.0f;
+  layer_routes(A, R);
+  const int h0 = blockIdx.x * 16 * RT;
+  const int IB = A.I / kScaleBlock;
+  const int64_t all = (int64_t)R.count * IB;
+  int64_t b = all * wave / kLayerDownWaves;
+  const int64_t end = all * (wave + 1) / kLayerDownWaves;
+  while (b < end) {
+    const int d = (int)(b / IB), k0 = (int)(b - (int64_t)d * IB);
+    const int k1 = (int)min((int64_t)IB, end - (int64_t)d * IB);
+    const int e = __builtin_amdgcn_readfirstlane(R.experts[d]);
+    const LayerMembers M = layer_members(A, R, e);
+    for (int c0 = 0; c0 < M.n; c0 += NT * 16) layer_down_part<RT, NT>(A, M, e, h0, k0, k1, c0, sums[wave]);
+    b = (int64_t)d * IB + k1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < A.tokens * RT * 8; i += kLayerDownWaves * kWave) {
+    float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLayerDownWaves; ++w) {
+      v0 += sums[w][2 * i];
+      v1 += sums[w][2 * i + 1];
+    }
+    const int t = i / (RT * 8), c = (i - t * RT * 8) * 2;
+    *reinterpret_cast<uint32_t*>(A.out + (int64_t)t * A.H + h0 + c) = pack_bf16(v0, v1);
+  }
+}
+
+}  // namespace
+
+int launch_layer_ll(const Dims& D, const uint16_t* x, const int* idx, const float* w, const uint8_t* w13_q,
+                    const float* w13_s, const uint8_t* w2_q, const float* w2_s, int I, uint16_t* out, uint32_t* flags,
+                    void* ws, hipStream_t st) {
+  const int tokens = D.N * D.T, slots = tokens * D.k;
+  uint16_t* a = static_cast<uint16_t*>(ws);
+  const LayerArgs A = {x, idx, w, w13_q, w13_s, w2_q, w2_s, out, flags, a, a + (int64_t)slots * I,
+                       tokens, slots, D.k, D.E, D.H, I};
+  const int active = slots < D.E ? slots : D.E;
+  const bool wide = slots > 8 * active;   // many tokens an expert: more columns a pass over the weights
+  int rc = launch("k_layer_up", wide ? k_layer_up<4> : k_layer_up<1>, dim3(I / 16, active),
+                  dim3(kLayerUpWaves * kWave), 0, st, A);
+  if (rc) return rc;
+  return launch("k_layer_down", wide ? k_layer_down<2, 4> : k_layer_down<2, 1>, dim3(D.H / 32),
+                dim3(kLayerDownWaves * kWave), 0, st, A);
+}
+
+}  // namespace moe

@@ -40,6 +40,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 64;
 constexpr int kMaxH = 32768;
 constexpr int kScaleBlock = 128;     // elements per fp32 scale
+constexpr int kLayerMaxTokens = 64;  // tokens of one moe_layer_ll call, all ranks together
 // Routing chunk: slots of one rank handled by one workgroup of the count
 // kernel; every wave takes a contiguous quarter, 64 slots per batch.  The
 // chunk is 256..4096 slots, chosen per shape so that small batches still
@@ -259,6 +260,16 @@ int launch_comb_send_partial(const Dims& D, const Ws& W, const uint16_t* y, cons
                              const float* w, uint16_t* comb, int cus, hipStream_t st);
 int launch_comb_recv_partial(const Dims& D, const Ws& W, const uint16_t* comb, const int* idx, const int* send_pos,
                              uint16_t* out, int cus, hipStream_t st);
+int launch_rmsnorm_quant(const Dims& D, const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps,
+                         uint16_t* res_out, uint16_t* y, uint8_t* y_q, float* y_s, hipStream_t st);
+int launch_grouped_gemm(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q, const float* w_s,
+                        const int* exp_off, int K, int F, uint16_t* y, int cus, hipStream_t st);
+int launch_grouped_gemm_swiglu(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q,
+                               const float* w_s, const int* exp_off, int K, int I, uint8_t* a_q, float* a_s, int cus,
+                               hipStream_t st);
+int launch_layer_ll(const Dims& D, const uint16_t* x, const int* idx, const float* w, const uint8_t* w13_q,
+                    const float* w13_s, const uint8_t* w2_q, const float* w2_s, int I, uint16_t* out, uint32_t* flags,
+                    void* ws, hipStream_t st);
 int launch_fill_u32(uint32_t* p, uint32_t v, int n, hipStream_t st);
 
 }  // namespace moe

@@ -329,6 +329,111 @@ int moe_combine_send_partial(const moe_shape *shape, const uint16_t *y_em, const
 int moe_combine_recv_partial(const moe_shape *shape, const uint16_t *comb, const int32_t *topk_idx,
                              const int32_t *send_pos, const void *ws, uint16_t *out, void *stream);
 
+/* ---------------------------------------------------------------- expert layer
+ *
+ * The operators between dispatch and combine and just before them: the norm
+ * that makes the tokens, the experts' products over the expert-major rows,
+ * and the whole layer for a few tokens.  They follow the conventions above:
+ * device pointers, one stream, contiguous arrays, host-side return codes.
+ *
+ * Weights are e4m3fn bytes with one fp32 scale for each block of 128 output
+ * features x 128 input features (the value is byte * scale).  "Gate and up"
+ * weights of an expert hold I gate features, then I up features.
+ */
+
+/*
+ * Root-mean-square norm of every token row, with the residual's addition in
+ * front and an 8-bit output behind:
+ *   r = x + residual,  n = r / sqrt(mean(r^2) + eps) * gamma
+ * in float32 (r is not rounded on the way), each output rounded once.
+ *   x         bf16 [N][T][H], 16-B aligned.
+ *   residual  bf16 [N][T][H] or NULL (r = x).
+ *   gamma     bf16 [H].
+ *   eps       finite and above 0, else MOE_EINVAL.
+ *   res_out   bf16 [N][T][H] out, r, or NULL.
+ *   y         bf16 [N][T][H] out, n, or NULL: the tokens of a dispatch.
+ *   y_q, y_s  fp8 e4m3fn [N][T][H] and fp32 [N][T][H/128] out, or both NULL:
+ *             n quantised as dispatch quantises (scale = amax/448, IEEE
+ *             division; a block of zeros has scale 0 and zero bytes), in the
+ *             layout moe_grouped_gemm reads (a shared expert, say).  A block
+ *             that holds an infinity or NaN gets that as its scale.
+ * At least one of y and y_q.  res_out and y may be x or residual themselves
+ * (same start), never a shifted overlap.  k, E and region_rows of the shape
+ * do not matter here.
+ */
+int moe_rmsnorm_quant(const moe_shape *shape, const uint16_t *x, const uint16_t *residual, const uint16_t *gamma,
+                      float eps, uint16_t *res_out, uint16_t *y, uint8_t *y_q, float *y_s, void *stream);
+
+/*
+ * The experts' product over expert-major rows: for every row i of expert e
+ *   y[i][f] = bf16_rne(sum_b x_s[i][b] * w_s[e][f/128][b] *
+ *                      sum_{c in block b} x_q[i][c] * w_q[e][f][c]),
+ * products exact and sums in float32.
+ *   x_q, x_s  fp8 e4m3fn [rows][K], 16-B aligned, and fp32 [rows][K/128], as
+ *             moe_dispatch_recv, moe_dispatch_direct, moe_grouped_gemm_swiglu
+ *             and (with N = E = k = 1, exp_off = {0, T}) moe_rmsnorm_quant
+ *             write them; rows = moe_recv_rows(shape).
+ *   w_q, w_s  fp8 e4m3fn [E][F][K], 16-B aligned, and fp32
+ *             [E][ceil(F/128)][K/128].
+ *   exp_off   int32 [N][E/N+1], from dispatch.  With packed regions rank d's
+ *             rows follow rank d-1's.
+ *   K, F      input and output features: K a multiple of 128, 128..32768; F a
+ *             multiple of 16, 16..32768, else MOE_EINVAL.  The shape's H does
+ *             not matter here, so one shape serves both products of a layer.
+ *   y         bf16 [rows][F] out, 16-B aligned: y_em of the combine.
+ * Rows that exp_off gives to no expert are neither read nor written; a row
+ * that a fixed region's overflow left without a token inside an expert's
+ * range gets the product of what x_q holds there (no combine reads it).
+ */
+int moe_grouped_gemm(const moe_shape *shape, const uint8_t *x_q, const float *x_s, const uint8_t *w_q,
+                     const float *w_s, const int32_t *exp_off, int32_t K, int32_t F, uint16_t *y, void *stream);
+
+/*
+ * The same product with gate and up weights and their activation behind it,
+ * quantised again: with g and u the float32 products of features f and I + f,
+ *   a[i][f] = g / (1 + exp(-g)) * u,
+ *   a_s[i][b] = amax over block b of 128 features / 448,  a_q = e4m3fn(a / a_s)
+ * (quantised from float32, by dispatch's rule).
+ *   w13_q, w13_s  fp8 e4m3fn [E][2*I][K], 16-B aligned, and fp32
+ *                 [E][2*I/128][K/128].
+ *   I             a multiple of 128, 128..32768, else MOE_EINVAL.
+ *   a_q, a_s      out, fp8 e4m3fn [rows][I], 16-B aligned, and fp32
+ *                 [rows][I/128]: x_q and x_s of the down product.
+ */
+int moe_grouped_gemm_swiglu(const moe_shape *shape, const uint8_t *x_q, const float *x_s, const uint8_t *w13_q,
+                            const float *w13_s, const int32_t *exp_off, int32_t K, int32_t I, uint8_t *a_q,
+                            float *a_s, void *stream);
+
+/*
+ * The whole layer for a few tokens (a decode step), from the tokens to the
+ * combined output in two launches, with no dispatched rows in between:
+ *   out[s][t] = bf16_rne(sum_j topk_w[s][t][j] * W2[e] (silu(Wg[e] x) * (Wu[e] x))),
+ *   e = topk_idx[s][t][j], x = tokens[s][t].
+ * It reads each weight of a chosen expert once.  Unlike the path through
+ * dispatch the tokens are not rounded to 8 bits: products are exact, sums in
+ * float32, and the weighted activation between the two products is held in
+ * 16 significand bits.
+ *   shape     N*T at most 64, else MOE_EINVAL; region_rows does not matter.
+ *   tokens    bf16 [N][T][H], 16-B aligned.
+ *   topk_idx, topk_w  int32, fp32 [N][T][k].  A slot with an id outside
+ *             [0, E) contributes nothing; an expert that a token names twice
+ *             counts with both weights; a token without a valid slot gets
+ *             zeros.
+ *   w13_q, w13_s  as for moe_grouped_gemm_swiglu with K = H.
+ *   w2_q, w2_s    fp8 e4m3fn [E][H][I], 16-B aligned, fp32 [E][H/128][I/128].
+ *   I         multiple of 128, 128..32768.
+ *   out       bf16 [N][T][H] out, 16-B aligned; may be the tokens' own memory.
+ *   flags     uint32 out, device, 4-B aligned: MOE_FLAG_BADID or 0, written
+ *             by every call.
+ *   ws        moe_layer_ll_workspace_bytes(shape, I) bytes, device, 256-B
+ *             aligned, no initialisation; holds nothing between calls.  Calls
+ *             that share it must be ordered.
+ */
+int64_t moe_layer_ll_workspace_bytes(const moe_shape *shape, int32_t I);
+int moe_layer_ll(const moe_shape *shape, const uint16_t *tokens, const int32_t *topk_idx, const float *topk_w,
+                 const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q, const float *w2_s, int32_t I,
+                 uint16_t *out, uint32_t *flags, void *ws, void *stream);
+
 /*
  * Wait for `stream`, return the sticky error bits accumulated in ws since the
  * last call (MOE_FLAG_*) through *flags, and clear them.  The only call that
