@@ -105,23 +105,34 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _arg(fn, name, t, dtypes, count=None, optional=False):
+def _arg(fn, name, t, dtypes, count, dev, optional=False):
     """A tensor's device pointer, after the checks a raw pointer does not
-    allow: type, contiguity, number of elements, and the current device
-    (kernels run on the current device's streams)."""
+    allow: type, contiguity, at least `count` elements, and memory of the
+    current device `dev` (kernels run on the current device's streams)."""
     if t is None and (optional or count == 0):
         return None
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.numel() >= count \
+            and t.get_device() == dev:
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} has type {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous")
-    if count is not None and t.numel() < count:
+    if t.numel() < count:
         raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {count}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
-    return ctypes.c_void_p(t.data_ptr())
+    raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2   # -1 is the CPU's number
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
 
 
 _BF16 = (torch.bfloat16,)
@@ -223,37 +234,36 @@ def moe_combine_recv_partial(sh, comb, topk_idx, send_pos, ws, out, stream=None)
                                                                     _stream(stream)))
 
 
-def _blocks(n: int) -> int:
-    return -(-n // 128)
-
-
 def moe_rmsnorm_quant(sh, x, residual, gamma, eps, res_out, y, y_q, y_s, stream=None):
-    f = "moe_rmsnorm_quant"
+    f, dev = "moe_rmsnorm_quant", _device()
     n = sh.N * sh.T * sh.H
     _check(f, lib.moe_rmsnorm_quant(
-        ctypes.byref(sh), _arg(f, "x", x, _BF16, n), _arg(f, "residual", residual, _BF16, n, True),
-        _arg(f, "gamma", gamma, _BF16, sh.H), eps, _arg(f, "res_out", res_out, _BF16, n, True),
-        _arg(f, "y", y, _BF16, n, True), _arg(f, "y_q", y_q, _F8, n, True),
-        _arg(f, "y_s", y_s, _F32, n // 128, True), _stream(stream)))
+        ctypes.byref(sh), _arg(f, "x", x, _BF16, n, dev), _arg(f, "residual", residual, _BF16, n, dev, True),
+        _arg(f, "gamma", gamma, _BF16, sh.H if n else 0, dev), eps, _arg(f, "res_out", res_out, _BF16, n, dev, True),
+        _arg(f, "y", y, _BF16, n, dev, True), _arg(f, "y_q", y_q, _F8, n, dev, True),
+        _arg(f, "y_s", y_s, _F32, n // 128, dev, True), _raw_stream(stream, dev)))
 
 
 def moe_grouped_gemm(sh, x_q, x_s, w_q, w_s, exp_off, K, F, y, stream=None):
-    f = "moe_grouped_gemm"
-    rows = moe_recv_rows(sh)
+    f, dev = "moe_grouped_gemm", _device()
+    rows, kb = moe_recv_rows(sh), K // 128
+    E = sh.E if sh.T else 0
     _check(f, lib.moe_grouped_gemm(
-        ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K), _arg(f, "x_s", x_s, _F32, rows * (K // 128)),
-        _arg(f, "w_q", w_q, _F8, sh.E * F * K), _arg(f, "w_s", w_s, _F32, sh.E * _blocks(F) * (K // 128)),
-        _arg(f, "exp_off", exp_off, _I32, sh.N + sh.E), K, F, _arg(f, "y", y, _BF16, rows * F), _stream(stream)))
+        ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K, dev), _arg(f, "x_s", x_s, _F32, rows * kb, dev),
+        _arg(f, "w_q", w_q, _F8, E * F * K, dev), _arg(f, "w_s", w_s, _F32, E * -(-F // 128) * kb, dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, F, _arg(f, "y", y, _BF16, rows * F, dev),
+        _raw_stream(stream, dev)))
 
 
 def moe_grouped_gemm_swiglu(sh, x_q, x_s, w13_q, w13_s, exp_off, K, I, a_q, a_s, stream=None):  # noqa: E741
-    f = "moe_grouped_gemm_swiglu"
-    rows = moe_recv_rows(sh)
+    f, dev = "moe_grouped_gemm_swiglu", _device()
+    rows, kb, ib = moe_recv_rows(sh), K // 128, I // 128
+    E = sh.E if sh.T else 0
     _check(f, lib.moe_grouped_gemm_swiglu(
-        ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K), _arg(f, "x_s", x_s, _F32, rows * (K // 128)),
-        _arg(f, "w13_q", w13_q, _F8, sh.E * 2 * I * K), _arg(f, "w13_s", w13_s, _F32, sh.E * 2 * (I // 128) * (K // 128)),
-        _arg(f, "exp_off", exp_off, _I32, sh.N + sh.E), K, I, _arg(f, "a_q", a_q, _F8, rows * I),
-        _arg(f, "a_s", a_s, _F32, rows * (I // 128)), _stream(stream)))
+        ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K, dev), _arg(f, "x_s", x_s, _F32, rows * kb, dev),
+        _arg(f, "w13_q", w13_q, _F8, E * 2 * I * K, dev), _arg(f, "w13_s", w13_s, _F32, E * 2 * ib * kb, dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, I, _arg(f, "a_q", a_q, _F8, rows * I, dev),
+        _arg(f, "a_s", a_s, _F32, rows * ib, dev), _raw_stream(stream, dev)))
 
 
 def moe_layer_ll_workspace_bytes(sh: moe_shape, I: int) -> int:  # noqa: E741
@@ -263,16 +273,17 @@ def moe_layer_ll_workspace_bytes(sh: moe_shape, I: int) -> int:  # noqa: E741
 
 
 def moe_layer_ll(sh, tokens, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, I, out, flags, ws, stream=None):  # noqa: E741
-    f = "moe_layer_ll"
+    f, dev = "moe_layer_ll", _device()
     n, H = sh.N * sh.T, sh.H
-    need = moe_layer_ll_workspace_bytes(sh, I)
+    need = moe_layer_ll_workspace_bytes(sh, I) if n else 0
     wq, wsc = (sh.E * I * H, sh.E * (I // 128) * (H // 128)) if n else (0, 0)
     _check(f, lib.moe_layer_ll(
-        ctypes.byref(sh), _arg(f, "tokens", tokens, _BF16, n * H), _arg(f, "topk_idx", topk_idx, _I32, n * sh.k),
-        _arg(f, "topk_w", topk_w, _F32, n * sh.k), _arg(f, "w13_q", w13_q, _F8, 2 * wq),
-        _arg(f, "w13_s", w13_s, _F32, 2 * wsc), _arg(f, "w2_q", w2_q, _F8, wq), _arg(f, "w2_s", w2_s, _F32, wsc), I,
-        _arg(f, "out", out, _BF16, n * H), _arg(f, "flags", flags, (torch.int32, torch.uint32), 1),
-        _arg(f, "ws", ws, (torch.uint8,), need if n else 0), _stream(stream)))
+        ctypes.byref(sh), _arg(f, "tokens", tokens, _BF16, n * H, dev),
+        _arg(f, "topk_idx", topk_idx, _I32, n * sh.k, dev), _arg(f, "topk_w", topk_w, _F32, n * sh.k, dev),
+        _arg(f, "w13_q", w13_q, _F8, 2 * wq, dev), _arg(f, "w13_s", w13_s, _F32, 2 * wsc, dev),
+        _arg(f, "w2_q", w2_q, _F8, wq, dev), _arg(f, "w2_s", w2_s, _F32, wsc, dev), I,
+        _arg(f, "out", out, _BF16, n * H, dev), _arg(f, "flags", flags, (torch.int32, torch.uint32), 1, dev),
+        _arg(f, "ws", ws, (torch.uint8,), need, dev), _raw_stream(stream, dev)))
 
 
 def moe_status(ws, stream=None) -> int:

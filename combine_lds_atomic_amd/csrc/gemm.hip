@@ -178,6 +178,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   constexpr int kStage = (BM + BN) * kBK;
   __shared__ __align__(1024) unsigned char lds[S * kStage];
   __shared__ float sx[2][kXsChunk][BN];
+  __shared__ float sw[2][2][kXsChunk];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -225,39 +226,34 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
     for (int i = 0; i < LPS; ++i) load_lds16(src[i] + kb * kBK, dst + i * NW * 1024);
   };
 
-  // ---- token scales, kXsChunk K steps at a time through registers
-  constexpr int kXsPer = BN * kXsChunk / THREADS > 0 ? BN * kXsChunk / THREADS : 1;   // scales of a thread
+  // ---- scales, kXsChunk K steps at a time through registers into LDS: a
+  // scale loaded where it is needed would wait for every load in front of it,
+  // the next stage's among them.  A tile has two blocks of weight rows: gate
+  // and up, or (BM = 256) the lower and the upper 128 features.
+  constexpr int kXsPer = BN * kXsChunk / THREADS > 0 ? BN * kXsChunk / THREADS : 1;   // token scales of a thread
   constexpr int kXsThreads = BN * kXsChunk / kXsPer;
   constexpr int kXsGroups = kXsChunk / kXsPer;
-  static_assert(kXsPer <= kXsChunk, "");
-  float xs[kXsPer];
-  const int xtok = threadIdx.x / kXsGroups, xk = (threadIdx.x % kXsGroups) * kXsPer;
-  auto xs_load = [&](int kb0) {
-    if (kXsThreads == THREADS || threadIdx.x < kXsThreads) {
-      const float* p = A.x_s + (int64_t)(T.row + min(xtok, T.n - 1)) * KB;
-#pragma unroll
-      for (int i = 0; i < kXsPer; ++i) xs[i] = p[min(kb0 + xk + i, KB - 1)];
-    }
-  };
-  auto xs_store = [&](int kb0) {
-    if (kXsThreads == THREADS || threadIdx.x < kXsThreads) {
-#pragma unroll
-      for (int i = 0; i < kXsPer; ++i) sx[(kb0 / kXsChunk) & 1][xk + i][xtok] = xs[i];
-    }
-  };
-
-  // ---- weight scales: one (plain) or two (gate, up) per wave and K step
+  static_assert(kXsPer <= kXsChunk && THREADS >= 2 * kXsChunk, "");
   const int nfb = (A.F + kScaleBlock - 1) / kScaleBlock;
-  const float* ws0;
-  const float* ws1;
-  if (SW) {
-    ws0 = A.w_s + ((int64_t)T.e * 2 * nfb + ft) * KB;
-    ws1 = ws0 + (int64_t)nfb * KB;
-  } else {
-    const int fb = min((ft * BM + wm * (BM / WM)) / kScaleBlock, nfb - 1);
-    ws0 = A.w_s + ((int64_t)T.e * nfb + fb) * KB;
-    ws1 = ws0;
-  }
+  float xs[kXsPer], wsc;
+  const int xtok = threadIdx.x / kXsGroups, xk = (threadIdx.x % kXsGroups) * kXsPer;
+  const int wk = threadIdx.x % kXsChunk, wb = threadIdx.x / kXsChunk;   // the first 16 threads
+  const float* wsp = A.w_s + (SW ? ((int64_t)T.e * 2 + (wb & 1)) * nfb + ft
+                                 : (int64_t)T.e * nfb + min(ft * (BM / kScaleBlock) + (wb & 1), nfb - 1)) * KB;
+  const float* xsp = A.x_s + (int64_t)(T.row + min(xtok, T.n - 1)) * KB;
+  auto scales_load = [&](int kb0) {
+    if (kXsThreads == THREADS || threadIdx.x < kXsThreads)
+#pragma unroll
+      for (int i = 0; i < kXsPer; ++i) xs[i] = xsp[min(kb0 + xk + i, KB - 1)];
+    if (threadIdx.x < 2 * kXsChunk) wsc = wsp[min(kb0 + wk, KB - 1)];
+  };
+  auto scales_store = [&](int kb0) {
+    const int buf = (kb0 / kXsChunk) & 1;
+    if (kXsThreads == THREADS || threadIdx.x < kXsThreads)
+#pragma unroll
+      for (int i = 0; i < kXsPer; ++i) sx[buf][xk + i][xtok] = xs[i];
+    if (threadIdx.x < 2 * kXsChunk) sw[buf][wb][wk] = wsc;
+  };
 
   v4f acc[MT][NT];
 #pragma unroll
@@ -265,8 +261,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0, 0, 0, 0};
 
-  xs_load(0);
-  xs_store(0);
+  scales_load(0);
+  scales_store(0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < KB) issue(s);
@@ -276,37 +272,46 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   const int lr = (lane & 15) * kBK;
   const int o0 = lr + (((lane >> 4) ^ (lane & 7)) << 4), o1 = lr + (((4 + (lane >> 4)) ^ (lane & 7)) << 4);
   const int tok0 = wn * (BN / WN) + (lane & 15);
+  // First LDS row of the wave's m-th tile of weight rows.
+  auto wrow = [&](int m) {
+    return SW ? (m < MT / 2 ? wm * (BF / WM) + m * 16 : BF + wm * (BF / WM) + (m - MT / 2) * 16)
+              : wm * (BM / WM) + m * 16;
+  };
+  const int wblk = SW ? 0 : wm * (BM / WM) / kScaleBlock;
 
   for (int kb = 0; kb < KB; ++kb) {
     if (S > 2 && kb + S - 1 <= KB) wait_and_barrier<(S - 2) * LPS>();
     else wait_and_barrier<0>();
+    const int ph = kb % kXsChunk, buf = (kb / kXsChunk) & 1;
+    if (ph == kXsChunk - 1 && kb + 1 < KB) scales_store(kb + 1);
     if (kb + S - 1 < KB) issue(kb + S - 1);
-    const int ph = kb % kXsChunk;
-    if (ph == 2 && kb - ph + kXsChunk < KB) xs_load(kb - ph + kXsChunk);
-    if (ph == kXsChunk - 1 && kb + 1 < KB) xs_store(kb + 1);
+    if (ph == 2 && kb - ph + kXsChunk < KB) scales_load(kb - ph + kXsChunk);
 
     const unsigned char* st = lds + (kb % S) * kStage;
-    const float s0 = ws0[kb], s1 = SW ? ws1[kb] : s0;
-    float sc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n] = sx[(kb / kXsChunk) & 1][ph][tok0 + n * 16];
-    Operand<SW> b[NT];
+    Operand<SW> b[NT], a[2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) b[n].load(st + (BM + wn * (BN / WN) + n * 16) * kBK, o0, o1);
+    a[0].load(st + wrow(0) * kBK, o0, o1);
+    float s0[NT], s1[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = SW ? (m < MT / 2 ? wm * (BF / WM) + m * 16 : BF + wm * (BF / WM) + (m - MT / 2) * 16)
-                         : wm * (BM / WM) + m * 16;
-      Operand<SW> a;
-      a.load(st + row * kBK, o0, o1);
-      v4f pr[NT];
-      multiply(a, b, pr);
+    for (int n = 0; n < NT; ++n) {
+      const float x = sx[buf][ph][tok0 + n * 16];
+      s0[n] = x * sw[buf][wblk][ph];
+      s1[n] = SW ? x * sw[buf][1][ph] : s0[n];
+    }
+    // Tile m's products run while the sums take tile m - 1's and tile m + 1's
+    // operand is read.
+    v4f pr[2][NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float s = sc[n] * (SW && m >= MT / 2 ? s1 : s0);
+    for (int m = 0; m <= MT; ++m) {
+      if (m + 1 < MT) a[(m + 1) & 1].load(st + wrow(m + 1) * kBK, o0, o1);
+      if (m < MT) multiply(a[m & 1], b, pr[m & 1]);
+      if (m > 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = __builtin_fmaf(pr[n][i], s, acc[m][n][i]);
-      }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[m - 1][n][i] = __builtin_fmaf(pr[(m - 1) & 1][n][i], m - 1 < MT / 2 ? s0[n] : s1[n], acc[m - 1][n][i]);
     }
   }
 

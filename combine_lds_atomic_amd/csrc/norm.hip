@@ -49,6 +49,11 @@ __device__ __forceinline__ void unpack8(const v4u& a, float* f) {
 // idle).  One wave per row if WAVE (no barrier), otherwise a workgroup.
 // Every read of a row comes before the first write to it, so outputs may be
 // the inputs' own memory.
+//
+// Bound by HBM: 4 H bytes in and 5 H + H/32 out per row.  Two units a thread
+// (448 threads at H = 7168) measured 679 us on 65536 rows, 6.25 TB/s, against
+// a plain copy's 6.6; one unit 815 us, four 677, a wave per row (14 units)
+// 790.  On 4096 rows 53, 59, 56 and 70 us.
 template <int U, bool WAVE>
 __global__ __launch_bounds__(WAVE ? kNormWaves* kWave : kNormMaxThreads) void k_rmsnorm_quant(NormArgs A) {
   __shared__ float part[kNormMaxThreads / kWave];
@@ -131,15 +136,12 @@ int launch_rmsnorm_quant(const Dims& D, const uint16_t* x, const uint16_t* resid
   const NormArgs A = {x, residual, gamma, res_out, y, y_q, y_s, eps, rows, D.H};
   const int units = D.H / 8;
   const char* name = "k_rmsnorm_quant";
+  const dim3 some((uint32_t)((rows + kNormWaves - 1) / kNormWaves)), all((uint32_t)rows);
   auto threads = [&](int u) { return dim3((units + u * kWave - 1) / (u * kWave) * kWave); };
-  if (units <= kWave) {
-    const uint32_t grid = (uint32_t)((rows + kNormWaves - 1) / kNormWaves);
-    return launch(name, k_rmsnorm_quant<1, true>, dim3(grid), dim3(kNormWaves * kWave), 0, st, A);
-  }
-  const dim3 grid((uint32_t)rows);
-  if (units <= kNormMaxThreads) return launch(name, k_rmsnorm_quant<1, false>, grid, threads(1), 0, st, A);
-  if (units <= 2 * kNormMaxThreads) return launch(name, k_rmsnorm_quant<2, false>, grid, threads(2), 0, st, A);
-  return launch(name, k_rmsnorm_quant<4, false>, grid, threads(4), 0, st, A);
+  if (units <= kWave) return launch(name, k_rmsnorm_quant<1, true>, some, dim3(kNormWaves * kWave), 0, st, A);
+  if (units <= 2 * kWave) return launch(name, k_rmsnorm_quant<2, true>, some, dim3(kNormWaves * kWave), 0, st, A);
+  if (units <= 2 * kNormMaxThreads) return launch(name, k_rmsnorm_quant<2, false>, all, threads(2), 0, st, A);
+  return launch(name, k_rmsnorm_quant<4, false>, all, threads(4), 0, st, A);
 }
 
 }  // namespace moe
