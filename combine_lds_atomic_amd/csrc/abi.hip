@@ -478,7 +478,7 @@ int64_t moe_layer_ll_workspace_bytes(const moe_shape* shape, int32_t I) {
   Dims D;
   const int rc = layer_dims(shape, I, &D);
   if (rc) return rc;
-  return (int64_t)up((size_t)D.N * D.TK * I * sizeof(uint32_t) + kAlign);
+  return layer_ll_workspace(D, I);
 }
 
 int moe_layer_ll(const moe_shape* shape, const uint16_t* tokens, const int32_t* topk_idx, const float* topk_w,

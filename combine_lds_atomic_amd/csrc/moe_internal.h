@@ -267,6 +267,7 @@ int launch_grouped_gemm(const Dims& D, const uint8_t* x_q, const float* x_s, con
 int launch_grouped_gemm_swiglu(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q,
                                const float* w_s, const int* exp_off, int K, int I, uint8_t* a_q, float* a_s, int cus,
                                hipStream_t st);
+int64_t layer_ll_workspace(const Dims& D, int I);
 int launch_layer_ll(const Dims& D, const uint16_t* x, const int* idx, const float* w, const uint8_t* w13_q,
                     const float* w13_s, const uint8_t* w2_q, const float* w2_s, int I, uint16_t* out, uint32_t* flags,
                     void* ws, hipStream_t st);
