@@ -7,6 +7,8 @@
 // with e the expert of row i.  k_grouped_gemm<..., false> rounds y to bf16;
 // k_grouped_gemm<..., true> takes features f and I + f as gate and up,
 // forms silu(gate) * up and quantises it per 128 features.
+#include <type_traits>
+
 #include "moe_internal.h"
 #include "quant_dev.h"
 
@@ -43,70 +45,86 @@ __device__ __forceinline__ int expert_rows(const GemmArgs& A, int e, int* off) {
   return b - a;
 }
 
-// The token tile number tt (tiles of BN rows, expert after expert) and the
-// total of tiles.  Every wave computes it for itself: lane i takes EPL
-// consecutive experts, so there is no barrier and no table in memory.
+// A workgroup's tile: up to BN rows of one expert and one block of features.
 struct Tile {
-  int e;      // expert
+  int e;      // expert, -1 for none
   int row;    // first row
   int n;      // rows, at most BN
+  int f;      // feature tile
 };
 
+// Tiles are numbered expert after expert; those of one expert token tile
+// fastest, in groups of up to 10 token tiles.  Each of the 8 XCDs takes one
+// contiguous share of the numbers (workgroup b runs on XCD b % 8), so the 32
+// compute units of an XCD work on some 3 x 10 tiles of one expert at a time
+// and most of their loads meet in its L2.  An expert's rows are split evenly
+// over its token tiles, in steps of 16.
+//
+// Every wave finds its tile by itself: lane i takes EPL consecutive experts,
+// so there is no barrier and no table in memory.
 template <int BN, int EPL>
-struct TileScan {
+__device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
+  const int lane = threadIdx.x & (kWave - 1);
   int n[EPL], off[EPL];
-  int rows_before, tiles_before, tiles;   // before this lane's experts; tiles of all experts
-
-  __device__ __forceinline__ void load(const GemmArgs& A) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int r = 0, t = 0;
+  int rows = 0, tiles = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      n[i] = expert_rows(A, min(e, A.E - 1), &off[i]);
-      if (e >= A.E) n[i] = 0;
-      r += n[i];
-      t += (n[i] + BN - 1) / BN;
-    }
-    int ri = r, ti = t;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int a = __shfl_up(ri, d), b = __shfl_up(ti, d);
-      if (lane >= d) {
-        ri += a;
-        ti += b;
-      }
-    }
-    rows_before = ri - r;
-    tiles_before = ti - t;
-    tiles = __builtin_amdgcn_readlane(ti, kWave - 1);
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * EPL + i;
+    n[i] = expert_rows(A, min(e, A.E - 1), &off[i]);
+    if (e >= A.E) n[i] = 0;
+    rows += n[i];
+    tiles += (n[i] + BN - 1) / BN;
   }
-
-  __device__ __forceinline__ Tile find(const GemmArgs& A, int tt) const {
-    const int lane = threadIdx.x & (kWave - 1);
-    int t = tiles_before, r = rows_before, e = -1, row = 0, m = 0;
+  int ri = rows, ti = tiles;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int c = (n[i] + BN - 1) / BN;
-      if (tt >= t && tt < t + c) {
-        const int ex = lane * EPL + i, skip = (tt - t) * BN;
-        const int cap = A.R ? A.R * (ex / A.L + 1) : A.rows;
-        e = ex;
-        row = min(max((A.R ? A.R * (ex / A.L) + off[i] : r) + skip, 0), cap);
-        m = min(min(n[i] - skip, BN), cap - row);
-      }
-      t += c;
-      r += n[i];
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int a = __shfl_up(ri, d), b = __shfl_up(ti, d);
+    if (lane >= d) {
+      ri += a;
+      ti += b;
     }
-    const unsigned long long who = __ballot(e >= 0);
-    const int src = who ? __builtin_ctzll(who) : 0;
-    Tile T;
-    T.e = __builtin_amdgcn_readlane(e, src);
-    T.row = __builtin_amdgcn_readlane(row, src);
-    T.n = __builtin_amdgcn_readlane(m, src);
-    return T;
   }
-};
+  Tile T = {-1, 0, 0, 0};
+  const int64_t total = (int64_t)__builtin_amdgcn_readlane(ti, kWave - 1) * nf;
+  const int64_t per = (total + 7) / 8;
+  const int64_t t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= per || t >= total) return T;
+  const int tt = (int)(t / nf);   // some token tile of the same expert
+  int r = ri - rows, first = ti - tiles, e = -1, row = 0, m = 0, c = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int ci = (n[i] + BN - 1) / BN;
+    if (tt >= first && tt < first + ci) {
+      e = lane * EPL + i;
+      row = A.R ? A.R * (e / A.L) + off[i] : r;
+      m = n[i];
+      c = ci;
+      break;
+    }
+    first += ci;
+    r += n[i];
+  }
+  const unsigned long long who = __ballot(e >= 0);
+  if (!who) return T;
+  const int src = __builtin_ctzll(who);
+  e = __builtin_amdgcn_readlane(e, src);
+  row = __builtin_amdgcn_readlane(row, src);
+  m = __builtin_amdgcn_readlane(m, src);
+  c = __builtin_amdgcn_readlane(c, src);
+  first = __builtin_amdgcn_readlane(first, src);
+  constexpr int kGroup = 10;
+  const int groups = (c + kGroup - 1) / kGroup, size = (c + groups - 1) / groups;
+  int x = (int)(t - (int64_t)first * nf);      // number among the expert's tiles
+  const int g = x / (size * nf), g0 = g * size, gs = min(size, c - g0);
+  x -= g0 * nf;
+  const int tile = g0 + x % gs, share = min((m + c - 1) / c + 15 & ~15, BN);
+  const int cap = A.R ? A.R * (e / A.L + 1) : A.rows;
+  T.e = e;
+  T.f = x / gs;
+  T.row = min(max(row + tile * share, 0), cap);
+  T.n = min(min(m - tile * share, share), cap - T.row);
+  return T;
+}
 
 // 16 bytes per lane straight from global memory into LDS: lane i's bytes land
 // at dst + 16*i (dst wave-uniform).
@@ -172,8 +190,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;     // 16x16 tiles of a wave
   constexpr int kRowsPerLoad = kWave / 8;                  // 8 lanes of 16 bytes per row
   constexpr int LPS = (BM + BN) / kRowsPerLoad / NW;       // loads per wave and stage
-  static_assert((BM + BN) % (kRowsPerLoad * NW) == 0, "rows split evenly over the waves");
-  static_assert(BM % (kRowsPerLoad * NW) == 0 || NW * kRowsPerLoad > BM, "");
+  static_assert(BM % (kRowsPerLoad * NW) == 0 && BN % (kRowsPerLoad * NW) == 0, "rows split evenly over the waves");
   static_assert(!SW || BM == 2 * kScaleBlock, "a gate and an up half of one scale block");
   constexpr int kStage = (BM + BN) * kBK;
   __shared__ __align__(1024) unsigned char lds[S * kStage];
@@ -184,21 +201,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
 
-  // ---- which tile
-  TileScan<BN, EPL> scan;
-  scan.load(A);
   constexpr int BF = SW ? BM / 2 : BM;      // output features of a tile
-  const int nf = (A.F + BF - 1) / BF;
-  const int64_t total = (int64_t)scan.tiles * nf;
-  const int64_t per = (total + 7) / 8;
-  const int64_t t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || t >= total) return;
-  constexpr int GT = 8;
-  const int g = (int)(t / (GT * nf)), first = g * GT, gs = min(GT, scan.tiles - first);
-  const int rr = (int)(t - (int64_t)g * GT * nf);
-  const int ft = rr / gs, tt = first + rr % gs;
-  const Tile T = scan.find(A, tt);
-  if (T.e < 0 || T.n <= 0) return;
+  const Tile T = find_tile<BN, EPL>(A, (A.F + BF - 1) / BF);
+  if (T.n <= 0) return;
+  const int ft = T.f;
 
   const int KB = A.K / kBK;
   const int wrows = SW ? 2 * A.F : A.F;     // weight rows of an expert
@@ -208,22 +214,20 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   // ---- this lane's source of each of its loads: LDS row R (weights first,
   // then tokens), 16-byte position p of the row holds chunk p ^ (R & 7), so
   // that the 8 lanes of a ds_read_b128 phase hit 8 different bank groups.
-  const uint8_t* src[LPS];
+  constexpr int kWLoads = BM / kRowsPerLoad / NW;
+  uint32_t src[LPS];   // F * K <= 2^30, and twice that with gate and up
 #pragma unroll
   for (int i = 0; i < LPS; ++i) {
     const int R = (i * NW + wave) * kRowsPerLoad + (lane >> 3);
-    const int c = ((lane & 7) ^ (R & 7)) * 16;
-    if (R < BM) {
-      int f = SW ? (R < BF ? ft * BF + R : A.F + ft * BF + R - BF) : min(ft * BF + R, A.F - 1);
-      src[i] = wbase + (int64_t)f * A.K + c;
-    } else {
-      src[i] = xbase + (int64_t)min(R - BM, T.n - 1) * A.K + c;
-    }
+    const int f = SW ? (R < BF ? ft * BF + R : A.F + ft * BF + R - BF) : min(ft * BF + R, A.F - 1);
+    const int row = i < kWLoads ? f : min(R - BM, T.n - 1);
+    src[i] = (uint32_t)row * (uint32_t)A.K + ((lane & 7) ^ (R & 7)) * 16;
   }
   auto issue = [&](int kb) {
     unsigned char* dst = lds + (kb % S) * kStage + wave * 1024;
+    const uint8_t *wk = wbase + kb * kBK, *xk = xbase + kb * kBK;
 #pragma unroll
-    for (int i = 0; i < LPS; ++i) load_lds16(src[i] + kb * kBK, dst + i * NW * 1024);
+    for (int i = 0; i < LPS; ++i) load_lds16((i < kWLoads ? wk : xk) + src[i], dst + i * NW * 1024);
   };
 
   // ---- scales, kXsChunk K steps at a time through registers into LDS: a
@@ -271,7 +275,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   // a 16-row tile; row & 7 = lane & 7 in every tile.
   const int lr = (lane & 15) * kBK;
   const int o0 = lr + (((lane >> 4) ^ (lane & 7)) << 4), o1 = lr + (((4 + (lane >> 4)) ^ (lane & 7)) << 4);
-  const int tok0 = wn * (BN / WN) + (lane & 15);
+  // The wave's n-th tile of tokens is tile n * WN + wn, so that the waves of a
+  // short tile have the same number of them to one; those behind the last row
+  // are left out.
+  const int tok0 = wn * 16 + (lane & 15);
+  const int live = min(max(((T.n + 15) / 16 - wn + WN - 1) / WN, 0), NT);
   // First LDS row of the wave's m-th tile of weight rows.
   auto wrow = [&](int m) {
     return SW ? (m < MT / 2 ? wm * (BF / WM) + m * 16 : BF + wm * (BF / WM) + (m - MT / 2) * 16)
@@ -279,47 +287,58 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   };
   const int wblk = SW ? 0 : wm * (BM / WM) / kScaleBlock;
 
-  for (int kb = 0; kb < KB; ++kb) {
-    if (S > 2 && kb + S - 1 <= KB) wait_and_barrier<(S - 2) * LPS>();
-    else wait_and_barrier<0>();
-    const int ph = kb % kXsChunk, buf = (kb / kXsChunk) & 1;
-    if (ph == kXsChunk - 1 && kb + 1 < KB) scales_store(kb + 1);
-    if (kb + S - 1 < KB) issue(kb + S - 1);
-    if (ph == 2 && kb - ph + kXsChunk < KB) scales_load(kb - ph + kXsChunk);
-
-    const unsigned char* st = lds + (kb % S) * kStage;
-    Operand<SW> b[NT], a[2];
+  auto steps = [&](auto nl) {
+    constexpr int NL = decltype(nl)::value;
+    for (int kb = 0; kb < KB; ++kb) {
+      if (S > 2 && kb + S - 1 <= KB) wait_and_barrier<(S - 2) * LPS>();
+      else wait_and_barrier<0>();
+      const int ph = kb % kXsChunk, buf = (kb / kXsChunk) & 1;
+      if (ph == kXsChunk - 1 && kb + 1 < KB) scales_store(kb + 1);
+      if (kb + S - 1 < KB) issue(kb + S - 1);
+      if (ph == 2 && kb - ph + kXsChunk < KB) scales_load(kb - ph + kXsChunk);
+      if constexpr (NL > 0) {
+        const unsigned char* st = lds + (kb % S) * kStage;
+        Operand<SW> b[NL], a[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) b[n].load(st + (BM + wn * (BN / WN) + n * 16) * kBK, o0, o1);
-    a[0].load(st + wrow(0) * kBK, o0, o1);
-    float s0[NT], s1[NT];
+        for (int n = 0; n < NL; ++n) b[n].load(st + (BM + (n * WN + wn) * 16) * kBK, o0, o1);
+        a[0].load(st + wrow(0) * kBK, o0, o1);
+        float s0[NL], s1[NL];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float x = sx[buf][ph][tok0 + n * 16];
-      s0[n] = x * sw[buf][wblk][ph];
-      s1[n] = SW ? x * sw[buf][1][ph] : s0[n];
+        for (int n = 0; n < NL; ++n) {
+          const float x = sx[buf][ph][tok0 + n * WN * 16];
+          s0[n] = x * sw[buf][wblk][ph];
+          s1[n] = SW ? x * sw[buf][1][ph] : s0[n];
+        }
+        // Tile m's products run while the sums take tile m - 1's and tile
+        // m + 1's operand is read.
+        v4f pr[2][NL];
+#pragma unroll
+        for (int m = 0; m <= MT; ++m) {
+          if (m + 1 < MT) a[(m + 1) & 1].load(st + wrow(m + 1) * kBK, o0, o1);
+          if (m < MT) multiply(a[m & 1], b, pr[m & 1]);
+          if (m > 0)
+#pragma unroll
+            for (int n = 0; n < NL; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[m - 1][n][i] =
+                    __builtin_fmaf(pr[(m - 1) & 1][n][i], m - 1 < MT / 2 ? s0[n] : s1[n], acc[m - 1][n][i]);
+        }
+      }
     }
-    // Tile m's products run while the sums take tile m - 1's and tile m + 1's
-    // operand is read.
-    v4f pr[2][NT];
-#pragma unroll
-    for (int m = 0; m <= MT; ++m) {
-      if (m + 1 < MT) a[(m + 1) & 1].load(st + wrow(m + 1) * kBK, o0, o1);
-      if (m < MT) multiply(a[m & 1], b, pr[m & 1]);
-      if (m > 0)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[m - 1][n][i] = __builtin_fmaf(pr[(m - 1) & 1][n][i], m - 1 < MT / 2 ? s0[n] : s1[n], acc[m - 1][n][i]);
-    }
-  }
+  };
+  static_assert(NT <= 4, "a loop for each number of live tiles");
+  if (live == NT) steps(std::integral_constant<int, NT>());
+  else if (NT > 3 && live == 3) steps(std::integral_constant<int, NT < 3 ? NT : 3>());
+  else if (NT > 2 && live == 2) steps(std::integral_constant<int, NT < 2 ? NT : 2>());
+  else if (NT > 1 && live == 1) steps(std::integral_constant<int, 1>());
+  else steps(std::integral_constant<int, 0>());
 
   // ---- epilogue: lane holds features row + 4*(lane/16) + i of token tok0 + 16n
   if constexpr (!SW) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int tok = tok0 + n * 16;
+      const int tok = tok0 + n * WN * 16;
       if (tok >= T.n) continue;
       uint16_t* yr = A.y + (int64_t)(T.row + tok) * A.F;
 #pragma unroll
@@ -347,12 +366,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
         }
       am = max(am, __shfl_xor(am, 16));
       am = max(am, __shfl_xor(am, 32));
-      if (lane < 16) red[wm * BN + tok0 + n * 16] = am;
+      if (lane < 16) red[wm * BN + tok0 + n * WN * 16] = am;
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int tok = tok0 + n * 16;
+      const int tok = tok0 + n * WN * 16;
       int am = 0;
 #pragma unroll
       for (int w = 0; w < WM; ++w) am = max(am, red[w * BN + tok]);
