@@ -32,6 +32,7 @@ struct GemmArgs {
   int N, L, E, R;   // ranks, experts per rank, experts, fixed region rows (0 = packed)
   int rows;         // rows of the arrays
   int K, F;         // input features, output features
+  int bn;           // rows of a tile at most (a multiple of 16, no more than the kernel's BN)
 };
 
 // Rows of expert e (rank d, l-th of the rank), and in *off its offset inside
@@ -45,11 +46,11 @@ __device__ __forceinline__ int expert_rows(const GemmArgs& A, int e, int* off) {
   return b - a;
 }
 
-// A workgroup's tile: up to BN rows of one expert and one block of features.
+// A workgroup's tile: up to A.bn rows of one expert and one block of features.
 struct Tile {
   int e;      // expert, -1 for none
   int row;    // first row
-  int n;      // rows, at most BN
+  int n;      // rows, at most A.bn
   int f;      // feature tile
 };
 
@@ -62,7 +63,7 @@ struct Tile {
 //
 // Every wave finds its tile by itself: lane i takes EPL consecutive experts,
 // so there is no barrier and no table in memory.
-template <int BN, int EPL>
+template <int EPL>
 __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
   const int lane = threadIdx.x & (kWave - 1);
   int n[EPL], off[EPL];
@@ -73,7 +74,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
     n[i] = expert_rows(A, min(e, A.E - 1), &off[i]);
     if (e >= A.E) n[i] = 0;
     rows += n[i];
-    tiles += (n[i] + BN - 1) / BN;
+    tiles += (n[i] + A.bn - 1) / A.bn;
   }
   int ri = rows, ti = tiles;
 #pragma unroll
@@ -93,7 +94,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
   int r = ri - rows, first = ti - tiles, e = -1, row = 0, m = 0, c = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int ci = (n[i] + BN - 1) / BN;
+    const int ci = (n[i] + A.bn - 1) / A.bn;
     if (tt >= first && tt < first + ci) {
       e = lane * EPL + i;
       row = A.R ? A.R * (e / A.L) + off[i] : r;
@@ -117,7 +118,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
   int x = (int)(t - (int64_t)first * nf);      // number among the expert's tiles
   const int g = x / (size * nf), g0 = g * size, gs = min(size, c - g0);
   x -= g0 * nf;
-  const int tile = g0 + x % gs, share = min((m + c - 1) / c + 15 & ~15, BN);
+  const int tile = g0 + x % gs, share = min(((m + c - 1) / c + 15) & ~15, A.bn);
   const int cap = A.R ? A.R * (e / A.L + 1) : A.rows;
   T.e = e;
   T.f = x / gs;
@@ -126,11 +127,17 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
   return T;
 }
 
-// 16 bytes per lane straight from global memory into LDS: lane i's bytes land
-// at dst + 16*i (dst wave-uniform).
-__device__ __forceinline__ void load_lds16(const uint8_t* src, unsigned char* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// 16 bytes per lane straight from global memory (base + the lane's offset)
+// into LDS: lane i's bytes land at dst + 16*i (dst wave-uniform).  There is no
+// register result, and the wait is wait_and_barrier's: with the builtin the
+// compiler waits for all of these loads before the next LDS read that follows
+// one, however far apart their buffers are.
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, unsigned char* dst) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(at)),
+               "v"(off), "s"(base)
+               : "m0");
 }
 
 // Wait until at most `Left` of this wave's LDS loads are on their way and all
@@ -140,28 +147,43 @@ __device__ __forceinline__ void wait_and_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(Left) : "memory");
 }
 
-// One lane's 32 bytes of a 16-row tile and K step, as the operand of a
-// 16x16 product over the step's 128 columns: the e4m3 bytes themselves
-// (Wide = false) or widened to bf16, which is exact.
+// One lane's 32 bytes of a 16-row tile and K step: as they are in LDS, and as
+// the operand of a 16x16 product over the step's 128 columns, which is the
+// e4m3 bytes themselves (Wide = false) or those widened to bf16 (exactly).
+struct Raw {
+  v4u lo, hi;
+  __device__ __forceinline__ void load(const unsigned char* p, int o0, int o1) {
+    lo = *reinterpret_cast<const v4u*>(p + o0);
+    hi = *reinterpret_cast<const v4u*>(p + o1);
+  }
+};
 template <bool Wide>
 struct Operand;
 template <>
 struct Operand<false> {
   v8i v;
   __device__ __forceinline__ void load(const unsigned char* p, int o0, int o1) {
-    const v4i lo = *reinterpret_cast<const v4i*>(p + o0), hi = *reinterpret_cast<const v4i*>(p + o1);
-    v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    Raw r;
+    r.load(p, o0, o1);
+    set(r);
+  }
+  __device__ __forceinline__ void set(const Raw& r) {
+    v = __builtin_shufflevector(__builtin_bit_cast(v4i, r.lo), __builtin_bit_cast(v4i, r.hi), 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
 template <>
 struct Operand<true> {
   v8bf v[4];
   __device__ __forceinline__ void load(const unsigned char* p, int o0, int o1) {
-    const v4u lo = *reinterpret_cast<const v4u*>(p + o0), hi = *reinterpret_cast<const v4u*>(p + o1);
-    v[0] = widen8(lo[0], lo[1]);
-    v[1] = widen8(lo[2], lo[3]);
-    v[2] = widen8(hi[0], hi[1]);
-    v[3] = widen8(hi[2], hi[3]);
+    Raw r;
+    r.load(p, o0, o1);
+    set(r);
+  }
+  __device__ __forceinline__ void set(const Raw& r) {
+    v[0] = widen8(r.lo[0], r.lo[1]);
+    v[1] = widen8(r.lo[2], r.lo[3]);
+    v[2] = widen8(r.hi[0], r.hi[1]);
+    v[3] = widen8(r.hi[2], r.hi[3]);
   }
 };
 
@@ -202,7 +224,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   const int wm = wave / WN, wn = wave % WN;
 
   constexpr int BF = SW ? BM / 2 : BM;      // output features of a tile
-  const Tile T = find_tile<BN, EPL>(A, (A.F + BF - 1) / BF);
+  const Tile T = find_tile<EPL>(A, (A.F + BF - 1) / BF);
   if (T.n <= 0) return;
   const int ft = T.f;
 
@@ -214,20 +236,31 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   // ---- this lane's source of each of its loads: LDS row R (weights first,
   // then tokens), 16-byte position p of the row holds chunk p ^ (R & 7), so
   // that the 8 lanes of a ds_read_b128 phase hit 8 different bank groups.
-  constexpr int kWLoads = BM / kRowsPerLoad / NW;
-  uint32_t src[LPS];   // F * K <= 2^30, and twice that with gate and up
+  constexpr int kWLoads = BM / kRowsPerLoad / NW, kStep = NW * kRowsPerLoad;
+  const uint32_t r0 = wave * kRowsPerLoad + (lane >> 3), c0 = ((lane & 7) ^ (r0 & 7)) * 16;
+  // Offsets of the weight loads: one for all where rows are whole blocks,
+  // else each with its row held below F (F * K <= 2^30).
+  uint32_t woff[SW ? 1 : kWLoads];
+  if constexpr (SW) {
+    woff[0] = r0 * (uint32_t)A.K + c0;
+  } else {
 #pragma unroll
-  for (int i = 0; i < LPS; ++i) {
-    const int R = (i * NW + wave) * kRowsPerLoad + (lane >> 3);
-    const int f = SW ? (R < BF ? ft * BF + R : A.F + ft * BF + R - BF) : min(ft * BF + R, A.F - 1);
-    const int row = i < kWLoads ? f : min(R - BM, T.n - 1);
-    src[i] = (uint32_t)row * (uint32_t)A.K + ((lane & 7) ^ (R & 7)) * 16;
+    for (int i = 0; i < kWLoads; ++i) woff[i] = min(ft * BF + r0 + i * kStep, (uint32_t)A.F - 1u) * (uint32_t)A.K + c0;
   }
-  auto issue = [&](int kb) {
+  // Loads [i0, i1) of step kb.
+  auto issue = [&](int kb, int i0, int i1) {
     unsigned char* dst = lds + (kb % S) * kStage + wave * 1024;
-    const uint8_t *wk = wbase + kb * kBK, *xk = xbase + kb * kBK;
 #pragma unroll
-    for (int i = 0; i < LPS; ++i) load_lds16((i < kWLoads ? wk : xk) + src[i], dst + i * NW * 1024);
+    for (int i = 0; i < LPS; ++i) {
+      if (i < i0 || i >= i1) continue;
+      if (i < kWLoads) {
+        const int64_t row = !SW ? 0 : ft * BF + (i < kWLoads / 2 ? i * kStep : A.F + (i - kWLoads / 2) * kStep);
+        load_lds16(wbase + row * A.K + kb * kBK, woff[SW ? 0 : i], dst + i * NW * 1024);
+      } else {   // the rows behind the tile's last are that row again
+        const uint32_t row = min(r0 + (i - kWLoads) * kStep, (uint32_t)T.n - 1u);
+        load_lds16(xbase + kb * kBK, __umul24(row, (uint32_t)A.K) + c0, dst + i * NW * 1024);
+      }
+    }
   };
 
   // ---- scales, kXsChunk K steps at a time through registers into LDS: a
@@ -269,7 +302,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   scales_store(0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
-    if (s < KB) issue(s);
+    if (s < KB) issue(s, 0, LPS);
 
   // Byte offset of this lane's 16 bytes (chunk lane/16, second chunk 4 on) in
   // a 16-row tile; row & 7 = lane & 7 in every tile.
@@ -294,35 +327,70 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
       else wait_and_barrier<0>();
       const int ph = kb % kXsChunk, buf = (kb / kXsChunk) & 1;
       if (ph == kXsChunk - 1 && kb + 1 < KB) scales_store(kb + 1);
-      if (kb + S - 1 < KB) issue(kb + S - 1);
       if (ph == 2 && kb - ph + kXsChunk < KB) scales_load(kb - ph + kXsChunk);
-      if constexpr (NL > 0) {
+      if constexpr (NL == 0) {
+        if (kb + S - 1 < KB) issue(kb + S - 1, 0, LPS);
+      } else {
+        // The next stage is asked for behind this step's first LDS reads: in
+        // front of them they would wait until all loads are issued.
         const unsigned char* st = lds + (kb % S) * kStage;
-        Operand<SW> b[NL], a[2];
+        const bool more = kb + S - 1 < KB;
+        Operand<SW> b[NL];
+        if constexpr (SW) {
+          // Registers are short (64 hold the tokens' operands), so one tile of
+          // weight rows after the other; the SIMD's other wave fills the gaps.
 #pragma unroll
-        for (int n = 0; n < NL; ++n) b[n].load(st + (BM + (n * WN + wn) * 16) * kBK, o0, o1);
-        a[0].load(st + wrow(0) * kBK, o0, o1);
-        float s0[NL], s1[NL];
+          for (int n = 0; n < NL; ++n) {
+            b[n].load(st + (BM + (n * WN + wn) * 16) * kBK, o0, o1);
+            if (n == 1) __builtin_amdgcn_sched_barrier(0);
+          }
+          Raw ra;
+          ra.load(st + wrow(0) * kBK, o0, o1);
+          float sc[NL];
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-          const float x = sx[buf][ph][tok0 + n * WN * 16];
-          s0[n] = x * sw[buf][wblk][ph];
-          s1[n] = SW ? x * sw[buf][1][ph] : s0[n];
-        }
-        // Tile m's products run while the sums take tile m - 1's and tile
-        // m + 1's operand is read.
-        v4f pr[2][NL];
+          for (int n = 0; n < NL; ++n) sc[n] = sx[buf][ph][tok0 + n * WN * 16];
+          const float w0 = sw[buf][0][ph], w1 = sw[buf][1][ph];
+          if (more) issue(kb + S - 1, 0, LPS / 2);
 #pragma unroll
-        for (int m = 0; m <= MT; ++m) {
-          if (m + 1 < MT) a[(m + 1) & 1].load(st + wrow(m + 1) * kBK, o0, o1);
-          if (m < MT) multiply(a[m & 1], b, pr[m & 1]);
-          if (m > 0)
+          for (int m = 0; m < MT; ++m) {
+            __builtin_amdgcn_sched_barrier(0);
+            Operand<SW> a;
+            a.set(ra);
+            if (m + 1 < MT) ra.load(st + wrow(m + 1) * kBK, o0, o1);
+            if (m == 0 && more) issue(kb + S - 1, LPS / 2, LPS);
+            v4f pr[NL];
+            multiply(a, b, pr);
 #pragma unroll
             for (int n = 0; n < NL; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                acc[m - 1][n][i] =
-                    __builtin_fmaf(pr[(m - 1) & 1][n][i], m - 1 < MT / 2 ? s0[n] : s1[n], acc[m - 1][n][i]);
+                acc[m][n][i] = __builtin_fmaf(pr[n][i], sc[n] * (m < MT / 2 ? w0 : w1), acc[m][n][i]);
+          }
+        } else {
+          // Tile m's products run while the sums take tile m - 1's and tile
+          // m + 1's operand is read.
+          Operand<SW> a[2];
+#pragma unroll
+          for (int n = 0; n < NL; ++n) b[n].load(st + (BM + (n * WN + wn) * 16) * kBK, o0, o1);
+          a[0].load(st + wrow(0) * kBK, o0, o1);
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) issue(kb + S - 1, 0, LPS);
+          __builtin_amdgcn_sched_barrier(0);
+          float sc[NL];
+#pragma unroll
+          for (int n = 0; n < NL; ++n) sc[n] = sx[buf][ph][tok0 + n * WN * 16] * sw[buf][wblk][ph];
+          v4f pr[2][NL];
+#pragma unroll
+          for (int m = 0; m <= MT; ++m) {
+            if (m + 1 < MT) a[(m + 1) & 1].load(st + wrow(m + 1) * kBK, o0, o1);
+            if (m < MT) multiply(a[m & 1], b, pr[m & 1]);
+            if (m > 0)
+#pragma unroll
+              for (int n = 0; n < NL; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  acc[m - 1][n][i] = __builtin_fmaf(pr[(m - 1) & 1][n][i], sc[n], acc[m - 1][n][i]);
+          }
         }
       }
     }
@@ -333,6 +401,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   else if (NT > 2 && live == 2) steps(std::integral_constant<int, NT < 2 ? NT : 2>());
   else if (NT > 1 && live == 1) steps(std::integral_constant<int, 1>());
   else steps(std::integral_constant<int, 0>());
+
+  // No load may be on its way to LDS that the epilogue, or another workgroup, uses.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // ---- epilogue: lane holds features row + 4*(lane/16) + i of token tok0 + 16n
   if constexpr (!SW) {
@@ -395,41 +466,59 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   }
 }
 
+// Rows of a tile: BN, or where the tiles do not fill the compute units twice,
+// the number of rows whose rounds over them cost least, a step's time being
+// about as bn + 48.
+int tile_rows(int64_t avg, int64_t active, int nf, int BN, int cus) {
+  auto tiles = [&](int bn) { return active * ((avg + bn - 1) / bn) * nf; };
+  if (tiles(BN) >= 2 * cus) return BN;
+  int best = BN;
+  int64_t least = INT64_MAX;
+  for (int bn = BN; bn >= 32; bn -= 16) {
+    const int64_t cost = (tiles(bn) + cus - 1) / cus * (bn + 48);
+    if (cost < least) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
+
 template <int BM, int BN, int WM, int WN, int S, bool SW>
-int launch_tile(const GemmArgs& A, int64_t slots, hipStream_t st) {
-  constexpr int BF = SW ? BM / 2 : BM;
+int launch_tile(GemmArgs A, int64_t slots, int cus, hipStream_t st) {
+  constexpr int BF = SW ? BM / 2 : BM, kThreadsHere = WM * WN * kWave;
   const int64_t active = slots < A.E ? slots : A.E;
-  const int64_t tiles = (slots / BN + active) * ((A.F + BF - 1) / BF);   // no fewer than the rows can need
+  const int nf = (A.F + BF - 1) / BF;
+  A.bn = tile_rows(slots / active, active, nf, BN, cus);
+  const int64_t tiles = (slots / A.bn + active) * nf;   // no fewer than the rows can need
   const int64_t grid = (tiles + 7) / 8 * 8;
-  if (grid > INT32_MAX) return MOE_ERANGE;
-  if (A.E <= 4 * kWave)
-    return launch("k_grouped_gemm", k_grouped_gemm<BM, BN, WM, WN, S, 4, SW>, dim3((uint32_t)grid), dim3(WM * WN * kWave),
-                  0, st, A);
-  return launch("k_grouped_gemm", k_grouped_gemm<BM, BN, WM, WN, S, 16, SW>, dim3((uint32_t)grid), dim3(WM * WN * kWave),
-                0, st, A);
+  if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
+  const auto k = A.E <= 4 * kWave ? k_grouped_gemm<BM, BN, WM, WN, S, 4, SW> : k_grouped_gemm<BM, BN, WM, WN, S, 16, SW>;
+  return launch("k_grouped_gemm", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 
 template <bool SW>
 int launch_any(const GemmArgs& A, int64_t slots, int cus, hipStream_t st) {
-  const int64_t active = slots < A.E ? slots : A.E;
-  const int64_t avg = slots / active;
-  if (avg > 256) return launch_tile<256, 256, 2, 4, 2, SW>(A, slots, st);
-  if (avg > 32) return launch_tile<256, 128, 4, 2, 3, SW>(A, slots, st);
-  return launch_tile<256, 32, 4, 1, 4, SW>(A, slots, st);
+  constexpr int BF = SW ? 128 : 256;
+  const int64_t active = slots < A.E ? slots : A.E, avg = slots / active;
+  const int64_t big = active * ((avg + 255) / 256) * ((A.F + BF - 1) / BF);   // tiles of 256 rows
+  if (avg > 256 && big >= 2 * cus) return launch_tile<256, 256, 2, 4, 2, SW>(A, slots, cus, st);
+  if (avg > 24) return launch_tile<256, 128, 4, 2, 3, SW>(A, slots, cus, st);
+  return launch_tile<256, 32, 4, 1, 2, SW>(A, slots, cus, st);
 }
 
 }  // namespace
 
 int launch_grouped_gemm(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q, const float* w_s,
                         const int* exp_off, int K, int F, uint16_t* y, int cus, hipStream_t st) {
-  GemmArgs A = {x_q, x_s, w_q, w_s, exp_off, y, nullptr, nullptr, D.N, D.L, D.E, D.R, D.rows, K, F};
+  GemmArgs A = {x_q, x_s, w_q, w_s, exp_off, y, nullptr, nullptr, D.N, D.L, D.E, D.R, D.rows, K, F, 0};
   return launch_any<false>(A, (int64_t)D.N * D.TK, cus, st);
 }
 
 int launch_grouped_gemm_swiglu(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q,
                                const float* w_s, const int* exp_off, int K, int I, uint8_t* a_q, float* a_s, int cus,
                                hipStream_t st) {
-  GemmArgs A = {x_q, x_s, w_q, w_s, exp_off, nullptr, a_q, a_s, D.N, D.L, D.E, D.R, D.rows, K, I};
+  GemmArgs A = {x_q, x_s, w_q, w_s, exp_off, nullptr, a_q, a_s, D.N, D.L, D.E, D.R, D.rows, K, I, 0};
   return launch_any<true>(A, (int64_t)D.N * D.TK, cus, st);
 }
 
