@@ -136,8 +136,7 @@ __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, un
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
                    __builtin_amdgcn_readfirstlane(at)),
-               "v"(off), "s"(base)
-               : "m0");
+               "v"(off), "s"(base));
 }
 
 // Wait until at most `Left` of this wave's LDS loads are on their way and all
@@ -206,15 +205,43 @@ __device__ __forceinline__ void multiply(const Operand<true>& a, const Operand<t
 constexpr int kBK = kScaleBlock;   // one K step = one scale block = one 16x16x128 product
 constexpr int kXsChunk = 8;        // K steps whose token scales are staged together
 
+// One workgroup forms BM weight rows x up to BN tokens of one expert: WM x WN
+// waves, each MT x NT matrix tiles of 16 x 16 with the weights as the left
+// operand, so a lane holds four neighbouring features of one token.  A K step
+// is one scale block: the step's products start from zero and join the
+// float32 sums with one fused multiply-add by x_s * w_s.  S stages of both
+// operands sit in LDS, filled by loads that bypass the registers.
+//
+// Two kinds of products:
+//   - plain form: e4m3 matrix instructions.  They add eight products at a time
+//     on a grid of 2^-13 of the largest one (measured with single products),
+//     which leaves 1.3e-5 of a row's norm; y's bf16 rounding leaves 1.7e-3.
+//   - SwiGLU form: its scales are float32 outputs, on which those 1.3e-5 would
+//     be seen, so the bytes are widened to bf16 (exactly) behind LDS and
+//     multiplied there, at half the instruction's rate and 1.5 to 2
+//     conversions per instruction (2e-7 against 64-bit sums).
+//
+// What bounds it on MI355X.  Plain form, 256 x 256, 2048 rows an expert: 9.6
+// ms for K = 2048 -> 7168 (1.60 PFLOP/s), 16.2 ms for 7168 -> 4096 (1.90);
+// a large library e4m3 product without block scales reaches 3.06.  LDS: the
+// waves read 192 KiB a step and the loads write 64, together the 2048 cycles
+// that the step's matrix instructions take; without the loads (a timing copy)
+// it is 2.5 PFLOP/s.  Direct weight loads to registers, prefetches into L2 and
+// a third stage with smaller tiles were slower.  SwiGLU form: 27.0 ms for 2048
+// rows an expert, K = 7168, I = 2048 (1.14 PFLOP/s; 29.3 with 160-row tiles);
+// a large library bf16 product reaches 1.5 to 1.6.  Its 128 x 64 tiles of a
+// wave fill the 256 registers that vector instructions can address, which
+// rules out larger ones.
 template <int BM, int BN, int WM, int WN, int S, int EPL, bool SW>
 __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   constexpr int NW = WM * WN, THREADS = NW * kWave;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;     // 16x16 tiles of a wave
   constexpr int kRowsPerLoad = kWave / 8;                  // 8 lanes of 16 bytes per row
-  constexpr int LPS = (BM + BN) / kRowsPerLoad / NW;       // loads per wave and stage
-  static_assert(BM % (kRowsPerLoad * NW) == 0 && BN % (kRowsPerLoad * NW) == 0, "rows split evenly over the waves");
+  constexpr int BNL = (BN + kRowsPerLoad * NW - 1) / (kRowsPerLoad * NW) * (kRowsPerLoad * NW);   // rows loaded
+  constexpr int LPS = (BM + BNL) / kRowsPerLoad / NW;      // loads per wave and stage
+  static_assert(BM % (kRowsPerLoad * NW) == 0, "rows split evenly over the waves");
   static_assert(!SW || BM == 2 * kScaleBlock, "a gate and an up half of one scale block");
-  constexpr int kStage = (BM + BN) * kBK;
+  constexpr int kStage = (BM + BNL) * kBK;
   __shared__ __align__(1024) unsigned char lds[S * kStage];
   __shared__ float sx[2][kXsChunk][BN];
   __shared__ float sw[2][2][kXsChunk];
@@ -267,10 +294,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   // scale loaded where it is needed would wait for every load in front of it,
   // the next stage's among them.  A tile has two blocks of weight rows: gate
   // and up, or (BM = 256) the lower and the upper 128 features.
-  constexpr int kXsPer = BN * kXsChunk / THREADS > 0 ? BN * kXsChunk / THREADS : 1;   // token scales of a thread
+  constexpr int kXsPer =   // token scales of a thread
+      BN * kXsChunk <= THREADS ? 1 : BN * kXsChunk % THREADS ? 4 : BN * kXsChunk / THREADS;
   constexpr int kXsThreads = BN * kXsChunk / kXsPer;
   constexpr int kXsGroups = kXsChunk / kXsPer;
-  static_assert(kXsPer <= kXsChunk && THREADS >= 2 * kXsChunk, "");
+  static_assert(kXsChunk % kXsPer == 0 && kXsThreads <= THREADS && THREADS >= 2 * kXsChunk, "");
   const int nfb = (A.F + kScaleBlock - 1) / kScaleBlock;
   float xs[kXsPer], wsc;
   const int xtok = threadIdx.x / kXsGroups, xk = (threadIdx.x % kXsGroups) * kXsPer;
@@ -395,8 +423,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
       }
     }
   };
-  static_assert(NT <= 4, "a loop for each number of live tiles");
+  static_assert(NT <= 5, "a loop for each number of live tiles");
   if (live == NT) steps(std::integral_constant<int, NT>());
+  else if (NT > 4 && live == 4) steps(std::integral_constant<int, NT < 4 ? NT : 4>());
   else if (NT > 3 && live == 3) steps(std::integral_constant<int, NT < 3 ? NT : 3>());
   else if (NT > 2 && live == 2) steps(std::integral_constant<int, NT < 2 ? NT : 2>());
   else if (NT > 1 && live == 1) steps(std::integral_constant<int, 1>());
@@ -468,7 +497,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
 
 // Rows of a tile: BN, or where the tiles do not fill the compute units twice,
 // the number of rows whose rounds over them cost least, a step's time being
-// about as bn + 48.
+// about as bn + 48 (1337 rows of one expert, K = 7168 -> 4096: 96 rows, 61 us;
+// 67 us with 128).
 int tile_rows(int64_t avg, int64_t active, int nf, int BN, int cus) {
   auto tiles = [&](int bn) { return active * ((avg + bn - 1) / bn) * nf; };
   if (tiles(BN) >= 2 * cus) return BN;
@@ -497,13 +527,24 @@ int launch_tile(GemmArgs A, int64_t slots, int cus, hipStream_t st) {
   return launch("k_grouped_gemm", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 
+// The tile goes by the rows that an active expert has on average:
+//   - above 256, and enough tiles: 256 rows.  2048 rows an expert: plain 9.7 ms
+//     against 10.9 with the middle tile, SwiGLU 27.0 against 29.3.
+//   - up to 256: the middle tile, 128 rows and three stages for the plain form
+//     (128 rows an expert, K = 2048 -> 7168: 1.03 ms against 1.05 with 160
+//     rows and two stages), 160 rows for SwiGLU (K = 7168, I = 2048: 2.32 ms
+//     against 2.65 with 128 rows, which half of the experts exceed, and 2.51
+//     with 256).
+//   - up to 24: 32 rows in workgroups of 4 waves, two on a compute unit; the
+//     weights' stream is the bound (5 rows an expert, K = 2048: plain 99 us
+//     against 106, SwiGLU 188 against 216 for the best middle tile).
 template <bool SW>
 int launch_any(const GemmArgs& A, int64_t slots, int cus, hipStream_t st) {
   constexpr int BF = SW ? 128 : 256;
   const int64_t active = slots < A.E ? slots : A.E, avg = slots / active;
   const int64_t big = active * ((avg + 255) / 256) * ((A.F + BF - 1) / BF);   // tiles of 256 rows
   if (avg > 256 && big >= 2 * cus) return launch_tile<256, 256, 2, 4, 2, SW>(A, slots, cus, st);
-  if (avg > 24) return launch_tile<256, 128, 4, 2, 3, SW>(A, slots, cus, st);
+  if (avg > 24) return launch_tile<256, SW ? 160 : 128, 4, 2, SW ? 2 : 3, SW>(A, slots, cus, st);
   return launch_tile<256, 32, 4, 1, 2, SW>(A, slots, cus, st);
 }
 

@@ -151,15 +151,16 @@ def uneven(E, total, seed, zero_every=3):
     (4, 1024, 5, 8, 256, 128),          # the most experts
     (1, 1, 257, 1, 2176, 640),          # one row over a tile, 17 K steps
     (2, 4, 513, 2, 2048, 384),          # 16 K steps
+    (2, 8, 2000, 2, 384, 4096),         # enough tiles of 256 rows: the large tile
+    (4, 512, 19200, 2, 128, 256),       # the same with more than 256 experts
 ])
 def test_grouped_gemm_shapes(swiglu, N, E, T, k, K, F):
     log(f"gemm swiglu={swiglu} N={N} E={E} T={T} k={k} K={K} F={F}")
     run_gemm(N, E, uneven(E, N * T * k, T), K, F, T, k, swiglu=swiglu, seed=K)
 
 
-@pytest.mark.parametrize("F", [16, 48, 112, 144, 272, 400])
-@pytest.mark.parametrize("T", [3, 90, 600])
-def test_grouped_gemm_odd_features(F, T):
+@pytest.mark.parametrize("T,F", [(T, F) for T in (3, 90, 600) for F in (16, 48, 112, 144, 272, 400)] + [(8000, 4112)])
+def test_grouped_gemm_odd_features(T, F):
     log(f"gemm F={F} T={T}")
     run_gemm(1, 2, [T - 1, T + 1], 384, F, T, 2, seed=F)
 
@@ -443,3 +444,75 @@ def test_chain_in_a_graph_and_on_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     for t, v in zip(outs, want):
         assert torch.equal(t, v)
+
+
+# ------------------------------------------------------------------ large offsets
+
+def test_grouped_gemm_offsets_beyond_32_bits():
+    """Rows and weights behind the first 2^31 bytes: the ends of the arrays
+    against a plain product."""
+    g = gen(31)
+    T, K, F = 153000, 7168, 128                       # 306000 rows of 7168 bytes
+    sh = moe.shape(1, T, 128, 2, 2)
+    rows = moe.moe_recv_rows(sh)
+    log(f"gemm rows={rows} K={K} F={F}")
+    eo = make_groups(1, 2, [rows - 70, 70])
+    x_q = torch.randint(0, 0x70, (rows, K), dtype=torch.uint8, generator=g, device="cuda")
+    x_s = torch.rand((rows, K // 128), generator=g, device="cuda")
+    w_q, w_s = X.weights(2, F, K, g)
+    y = torch.empty((rows, F), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm(sh, x_q, x_s, w_q, w_s, eo, K, F, y)
+    groups = [(0, 0, 40), (0, rows - 110, 40), (1, rows - 70, 70)]
+    for sl, r, d in X.gemm(x_q, x_s, w_q, w_s, groups):
+        X.check_bf16(y[sl], r, d, str(sl))
+    del x_q, x_s, y
+    E, F, T = 40, 8192, 20                             # 2.35 GB of weights
+    log(f"gemm E={E} F={F} K={K}")
+    sh = moe.shape(1, T, 128, E, 2)
+    counts = [0] * E
+    counts[0], counts[E - 1] = 3, 37
+    eo = make_groups(1, E, counts)
+    x_q, x_s = X.quantise(torch.randn((40, K), generator=g, device="cuda"))
+    w_q = torch.randint(0, 0x70, (E, F, K), dtype=torch.uint8, generator=g, device="cuda")
+    w_s = torch.rand((E, F // 128, K // 128), generator=g, device="cuda") * 1e-3
+    y = torch.empty((40, F), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm(sh, x_q, x_s, w_q, w_s, eo, K, F, y)
+    for sl, r, d in X.gemm(x_q, x_s, w_q, w_s, [(0, 0, 3), (E - 1, 3, 37)]):
+        X.check_bf16(y[sl], r, d, str(sl))
+    q, s = torch.empty((40, F // 2), dtype=torch.uint8, device="cuda"), torch.empty((40, F // 256), device="cuda")
+    moe.moe_grouped_gemm_swiglu(sh, x_q, x_s, w_q, w_s, eo, K, F // 2, q, s)
+    for sl, a, da in X.swiglu(x_q, x_s, w_q, w_s, [(0, 0, 3), (E - 1, 3, 37)]):
+        X.check_quantised(q[sl], s[sl], a, da, str(sl))
+
+
+def test_layer_weights_beyond_32_bits():
+    N, T, H, E, k, I = 1, 3, 7168, 64, 2, 2560  # noqa: E741   2.35 GB of gate/up weights
+    log(f"layer E={E} H={H} I={I}")
+    g = gen(8)
+    x = torch.randn((N, T, H), generator=g, device="cuda").bfloat16()
+    idx = torch.tensor([[[E - 1, 0], [E - 2, E - 1], [1, E - 3]]], dtype=torch.int32, device="cuda")
+    w = torch.rand((N, T, k), generator=g, device="cuda")
+    f8 = lambda *s: torch.randint(0, 0x68, s, dtype=torch.uint8, generator=g, device="cuda")  # noqa: E731
+    w13_q, w2_q = f8(E, 2 * I, H) ^ (f8(E, 2 * I, H) & 1) << 7, f8(E, H, I) ^ (f8(E, H, I) & 1) << 7
+    w13_s = torch.rand((E, 2 * I // 128, H // 128), generator=g, device="cuda") * 1e-3
+    w2_s = torch.rand((E, H // 128, I // 128), generator=g, device="cuda") * 1e-3
+    a = (x, idx, w, w13_q, w13_s, w2_q, w2_s)
+    out, flags = run_layer(N, T, H, E, k, I, *a)
+    assert flags == 0
+    check_layer(out, N, T, H, k, *a)
+
+
+def test_norm_rows_beyond_32_bits():
+    T, H = 300000, 7168                               # 2.15e9 elements
+    log(f"norm T={T} H={H}")
+    g = gen(4)
+    sh = moe.shape(1, T, H, 1, 1)
+    x = torch.randn((1, T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.randn(H, generator=g, device="cuda").bfloat16()
+    y = torch.empty_like(x)
+    q, s = torch.empty((1, T, H), dtype=torch.uint8, device="cuda"), torch.empty((1, T, H // 128), device="cuda")
+    moe.moe_rmsnorm_quant(sh, x, None, gamma, 1e-6, None, y, q, s)
+    for sl in (slice(0, 20), slice(T - 20, T)):
+        _, n, rel = X.norm(x[0, sl], None, gamma, 1e-6)
+        X.check_bf16(y[0, sl], n, n.abs() * rel)
+        X.check_quantised(q[0, sl], s[0, sl], n, n.abs() * rel)
