@@ -132,11 +132,17 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
 // register result, and the wait is wait_and_barrier's: with the builtin the
 // compiler waits for all of these loads before the next LDS read that follows
 // one, however far apart their buffers are.
-__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, unsigned char* dst) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
-                   __builtin_amdgcn_readfirstlane(at)),
-               "v"(off), "s"(base));
+__device__ __forceinline__ uint32_t lds_address(const void* dst) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)dst);
+}
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, void* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_address(dst)), "v"(off),
+               "s"(base));
+}
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, void* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds_address(dst)), "v"(off),
+               "s"(base));
 }
 
 // Wait until at most `Left` of this wave's LDS loads are on their way and all
@@ -203,7 +209,8 @@ __device__ __forceinline__ void multiply(const Operand<true>& a, const Operand<t
 }
 
 constexpr int kBK = kScaleBlock;   // one K step = one scale block = one 16x16x128 product
-constexpr int kXsChunk = 8;        // K steps whose token scales are staged together
+constexpr int kXsChunk = 8;        // K steps whose scales are staged together
+static_assert(2 * kXsChunk <= kWave, "one lane a weight scale");
 
 // One workgroup forms BM weight rows x up to BN tokens of one expert: WM x WN
 // waves, each MT x NT matrix tiles of 16 x 16 with the weights as the left
@@ -243,8 +250,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   static_assert(!SW || BM == 2 * kScaleBlock, "a gate and an up half of one scale block");
   constexpr int kStage = (BM + BNL) * kBK;
   __shared__ __align__(1024) unsigned char lds[S * kStage];
-  __shared__ float sx[2][kXsChunk][BN];
-  __shared__ float sw[2][2][kXsChunk];
+  constexpr int XG = (BN + kWave - 1) / kWave, XI = kXsChunk * XG / NW;   // scale loads of a chunk, and of a wave
+  static_assert(kXsChunk * XG % NW == 0, "scale loads split evenly over the waves");
+  __shared__ float sx[2][kXsChunk][XG * kWave];
+  __shared__ float sw[2][kWave];   // [block][K step of the chunk], 16 of the 64
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -290,34 +299,26 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
     }
   };
 
-  // ---- scales, kXsChunk K steps at a time through registers into LDS: a
-  // scale loaded where it is needed would wait for every load in front of it,
-  // the next stage's among them.  A tile has two blocks of weight rows: gate
-  // and up, or (BM = 256) the lower and the upper 128 features.
-  constexpr int kXsPer =   // token scales of a thread
-      BN * kXsChunk <= THREADS ? 1 : BN * kXsChunk % THREADS ? 4 : BN * kXsChunk / THREADS;
-  constexpr int kXsThreads = BN * kXsChunk / kXsPer;
-  constexpr int kXsGroups = kXsChunk / kXsPer;
-  static_assert(kXsChunk % kXsPer == 0 && kXsThreads <= THREADS && THREADS >= 2 * kXsChunk, "");
+  // ---- scales, kXsChunk K steps at a time, by the same kind of loads: a
+  // scale loaded into a register where it is needed would wait for every load
+  // in front of it, the next stage's among them.  A tile has two blocks of
+  // weight rows: gate and up, or the lower and the upper 128 features.
   const int nfb = (A.F + kScaleBlock - 1) / kScaleBlock;
-  float xs[kXsPer], wsc;
-  const int xtok = threadIdx.x / kXsGroups, xk = (threadIdx.x % kXsGroups) * kXsPer;
-  const int wk = threadIdx.x % kXsChunk, wb = threadIdx.x / kXsChunk;   // the first 16 threads
-  const float* wsp = A.w_s + (SW ? ((int64_t)T.e * 2 + (wb & 1)) * nfb + ft
-                                 : (int64_t)T.e * nfb + min(ft * (BM / kScaleBlock) + (wb & 1), nfb - 1)) * KB;
-  const float* xsp = A.x_s + (int64_t)(T.row + min(xtok, T.n - 1)) * KB;
-  auto scales_load = [&](int kb0) {
-    if (kXsThreads == THREADS || threadIdx.x < kXsThreads)
-#pragma unroll
-      for (int i = 0; i < kXsPer; ++i) xs[i] = xsp[min(kb0 + xk + i, KB - 1)];
-    if (threadIdx.x < 2 * kXsChunk) wsc = wsp[min(kb0 + wk, KB - 1)];
-  };
-  auto scales_store = [&](int kb0) {
+  const int wb0 = SW ? ft : min(ft * 2, nfb - 1), wb1 = SW ? nfb + ft : min(ft * 2 + 1, nfb - 1);
+  const float* wsp = A.w_s + ((int64_t)T.e * (SW ? 2 : 1) * nfb + wb0) * KB;
+  const float* xsp = A.x_s + (int64_t)T.row * KB;
+  auto scales = [&](int kb0) {
     const int buf = (kb0 / kXsChunk) & 1;
-    if (kXsThreads == THREADS || threadIdx.x < kXsThreads)
 #pragma unroll
-      for (int i = 0; i < kXsPer; ++i) sx[buf][xk + i][xtok] = xs[i];
-    if (threadIdx.x < 2 * kXsChunk) sw[buf][wb][wk] = wsc;
+    for (int i = 0; i < XI; ++i) {
+      const int j = i * NW + wave, kk = j / XG, g = j - kk * XG;
+      const uint32_t tok = min(g * kWave + lane, T.n - 1);
+      load_lds4(xsp + min(kb0 + kk, KB - 1), __umul24(tok, (uint32_t)KB * 4u), &sx[buf][kk][g * kWave]);
+    }
+    if (wave == 0) {
+      const int kk = min(kb0 + (lane & (kXsChunk - 1)), KB - 1), blk = lane / kXsChunk & 1;
+      load_lds4(wsp, (uint32_t)(blk * (wb1 - wb0) * KB + kk) * 4u, &sw[buf][0]);
+    }
   };
 
   v4f acc[MT][NT];
@@ -326,8 +327,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0, 0, 0, 0};
 
-  scales_load(0);
-  scales_store(0);
+  scales(0);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < KB) issue(s, 0, LPS);
@@ -354,8 +354,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
       if (S > 2 && kb + S - 1 <= KB) wait_and_barrier<(S - 2) * LPS>();
       else wait_and_barrier<0>();
       const int ph = kb % kXsChunk, buf = (kb / kXsChunk) & 1;
-      if (ph == kXsChunk - 1 && kb + 1 < KB) scales_store(kb + 1);
-      if (ph == 2 && kb - ph + kXsChunk < KB) scales_load(kb - ph + kXsChunk);
+      // Asked for early enough that the wait of a step before theirs covers them, with any S.
+      if (ph == 1 && kb - ph + kXsChunk < KB) scales(kb - ph + kXsChunk);
       if constexpr (NL == 0) {
         if (kb + S - 1 < KB) issue(kb + S - 1, 0, LPS);
       } else {
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
           float sc[NL];
 #pragma unroll
           for (int n = 0; n < NL; ++n) sc[n] = sx[buf][ph][tok0 + n * WN * 16];
-          const float w0 = sw[buf][0][ph], w1 = sw[buf][1][ph];
+          const float w0 = sw[buf][ph], w1 = sw[buf][kXsChunk + ph];
           if (more) issue(kb + S - 1, 0, LPS / 2);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
           __builtin_amdgcn_sched_barrier(0);
           float sc[NL];
 #pragma unroll
-          for (int n = 0; n < NL; ++n) sc[n] = sx[buf][ph][tok0 + n * WN * 16] * sw[buf][wblk][ph];
+          for (int n = 0; n < NL; ++n) sc[n] = sx[buf][ph][tok0 + n * WN * 16] * sw[buf][wblk * kXsChunk + ph];
           v4f pr[2][NL];
 #pragma unroll
           for (int m = 0; m <= MT; ++m) {
