@@ -2,7 +2,9 @@
 MI355X).  Argument marshalling only: every function forwards torch tensors'
 device pointers and the current HIP stream to the C ABI of
 ``include/moe_ep.h`` under the same name; all computation happens in the HIP
-kernels.  Importing this module fails loudly if the library is not built.
+kernels.  The expert layer's functions also check each tensor's type,
+contiguity, size and device first (TypeError, ValueError).  Importing this
+module fails loudly if the library is not built.
 """
 from __future__ import annotations
 

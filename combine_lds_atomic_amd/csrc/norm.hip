@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kNormWaves = 4;          // rows of a workgroup when one wave takes a row
 constexpr int kNormMaxThreads = 1024;
+constexpr int64_t kNormLaunchRows = 1 << 21;   // rows of a launch: keeps grid.x * 1024 below 2^32
 
 struct NormArgs {
   const uint16_t* x;
@@ -53,7 +54,10 @@ __device__ __forceinline__ void unpack8(const v4u& a, float* f) {
 // Bound by HBM: 4 H bytes in and 5 H + H/32 out per row.  Two units a thread
 // (448 threads at H = 7168) measured 679 us on 65536 rows, 6.25 TB/s, against
 // a plain copy's 6.6; one unit 815 us, four 677, a wave per row (14 units)
-// 790.  On 4096 rows 53, 59, 56 and 70 us.
+// 790 (720 to 760 us for the first on other days).  On 4096 rows 53, 59, 56
+// and 70 us.  Several rows a workgroup, one after the other with gamma kept
+// and the next row's loads in flight, were slower: 744 us for one row, 784
+// for four, 866 for sixteen, in one run.
 template <int U, bool WAVE>
 __global__ __launch_bounds__(WAVE ? kNormWaves* kWave : kNormMaxThreads) void k_rmsnorm_quant(NormArgs A) {
   __shared__ float part[kNormMaxThreads / kWave];
@@ -133,15 +137,23 @@ __global__ __launch_bounds__(WAVE ? kNormWaves* kWave : kNormMaxThreads) void k_
 int launch_rmsnorm_quant(const Dims& D, const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps,
                          uint16_t* res_out, uint16_t* y, uint8_t* y_q, float* y_s, hipStream_t st) {
   const int64_t rows = (int64_t)D.N * D.T;
-  const NormArgs A = {x, residual, gamma, res_out, y, y_q, y_s, eps, rows, D.H};
   const int units = D.H / 8;
   const char* name = "k_rmsnorm_quant";
-  const dim3 some((uint32_t)((rows + kNormWaves - 1) / kNormWaves)), all((uint32_t)rows);
   auto threads = [&](int u) { return dim3((units + u * kWave - 1) / (u * kWave) * kWave); };
-  if (units <= kWave) return launch(name, k_rmsnorm_quant<1, true>, some, dim3(kNormWaves * kWave), 0, st, A);
-  if (units <= 2 * kWave) return launch(name, k_rmsnorm_quant<2, true>, some, dim3(kNormWaves * kWave), 0, st, A);
-  if (units <= 2 * kNormMaxThreads) return launch(name, k_rmsnorm_quant<2, false>, all, threads(2), 0, st, A);
-  return launch(name, k_rmsnorm_quant<4, false>, all, threads(4), 0, st, A);
+  for (int64_t r0 = 0; r0 < rows; r0 += kNormLaunchRows) {
+    const int64_t n = rows - r0 < kNormLaunchRows ? rows - r0 : kNormLaunchRows, at = r0 * D.H;
+    auto from = [](auto* p, int64_t i) { return p ? p + i : p; };
+    const NormArgs A = {x + at, from(residual, at), gamma, from(res_out, at), from(y, at), from(y_q, at),
+                        from(y_s, at / kScaleBlock), eps, n, D.H};
+    const dim3 some((uint32_t)((n + kNormWaves - 1) / kNormWaves)), all((uint32_t)n);
+    int rc;
+    if (units <= kWave) rc = launch(name, k_rmsnorm_quant<1, true>, some, dim3(kNormWaves * kWave), 0, st, A);
+    else if (units <= 2 * kWave) rc = launch(name, k_rmsnorm_quant<2, true>, some, dim3(kNormWaves * kWave), 0, st, A);
+    else if (units <= 2 * kNormMaxThreads) rc = launch(name, k_rmsnorm_quant<2, false>, all, threads(2), 0, st, A);
+    else rc = launch(name, k_rmsnorm_quant<4, false>, all, threads(4), 0, st, A);
+    if (rc != MOE_OK) return rc;
+  }
+  return MOE_OK;
 }
 
 }  // namespace moe

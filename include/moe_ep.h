@@ -381,6 +381,8 @@ int moe_rmsnorm_quant(const moe_shape *shape, const uint16_t *x, const uint16_t 
  *             multiple of 16, 16..32768, else MOE_EINVAL.  The shape's H does
  *             not matter here, so one shape serves both products of a layer.
  *   y         bf16 [rows][F] out, 16-B aligned: y_em of the combine.
+ * The output must not overlap an input.  A shape whose tiles do not fit one
+ * launch (2^32 threads; far beyond what the arrays would fit) is MOE_ERANGE.
  * Rows that exp_off gives to no expert are neither read nor written; a row
  * that a fixed region's overflow left without a token inside an expert's
  * range gets the product of what x_q holds there (no combine reads it).

@@ -516,3 +516,21 @@ def test_norm_rows_beyond_32_bits():
         _, n, rel = X.norm(x[0, sl], None, gamma, 1e-6)
         X.check_bf16(y[0, sl], n, n.abs() * rel)
         X.check_quantised(q[0, sl], s[0, sl], n, n.abs() * rel)
+
+
+def test_norm_more_rows_than_one_launch():
+    """Above 2^21 rows the call takes several launches."""
+    T, H = (1 << 21) + 3, 128
+    log(f"norm T={T} H={H}")
+    g = gen(6)
+    sh = moe.shape(1, T, H, 1, 1)
+    x, res = (torch.randn((1, T, H), generator=g, device="cuda").bfloat16() for _ in range(2))
+    gamma = torch.randn(H, generator=g, device="cuda").bfloat16()
+    r, y = torch.empty_like(x), torch.empty_like(x)
+    q, s = torch.empty((1, T, H), dtype=torch.uint8, device="cuda"), torch.empty((1, T, 1), device="cuda")
+    moe.moe_rmsnorm_quant(sh, x, res, gamma, 1e-6, r, y, q, s)
+    for sl in (slice(0, 9), slice((1 << 21) - 5, T)):
+        ref, n, rel = X.norm(x[0, sl], res[0, sl], gamma, 1e-6)
+        X.check_bf16(r[0, sl], ref, ref.abs() * X.U)
+        X.check_bf16(y[0, sl], n, n.abs() * rel)
+        X.check_quantised(q[0, sl], s[0, sl], n, n.abs() * rel)
