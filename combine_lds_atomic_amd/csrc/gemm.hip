@@ -228,17 +228,20 @@ static_assert(2 * kXsChunk <= kWave, "one lane a weight scale");
 //     multiplied there, at half the instruction's rate and 1.5 to 2
 //     conversions per instruction (2e-7 against 64-bit sums).
 //
-// What bounds it on MI355X.  Plain form, 256 x 256, 2048 rows an expert: 9.6
-// ms for K = 2048 -> 7168 (1.60 PFLOP/s), 16.2 ms for 7168 -> 4096 (1.90);
-// a large library e4m3 product without block scales reaches 3.06.  LDS: the
-// waves read 192 KiB a step and the loads write 64, together the 2048 cycles
-// that the step's matrix instructions take; without the loads (a timing copy)
-// it is 2.5 PFLOP/s.  Direct weight loads to registers, prefetches into L2 and
-// a third stage with smaller tiles were slower.  SwiGLU form: 27.0 ms for 2048
-// rows an expert, K = 7168, I = 2048 (1.14 PFLOP/s; 29.3 with 160-row tiles);
-// a large library bf16 product reaches 1.5 to 1.6.  Its 128 x 64 tiles of a
-// wave fill the 256 registers that vector instructions can address, which
-// rules out larger ones.
+// What bounds it on MI355X.  Plain form, 256 x 256, 2048 rows an expert: 9.5
+// ms for K = 2048 -> 7168 (1.62 PFLOP/s), 16.5 ms for 7168 -> 4096 (1.86);
+// a large library e4m3 product without block scales reaches 3.06.  The bound
+// is LDS: the waves read 192 KiB a step and the loads write 64, together the
+// 2048 cycles that the step's matrix instructions take; without the loads (a
+// timing copy) it is 2.5 PFLOP/s.  Weights loaded straight to registers,
+// prefetches into L2, smaller tiles with a third stage, and non-temporal
+// stores of y (11.4 ms) were slower.
+// SwiGLU form: 27.0 ms for 2048 rows an expert, K = 7168, I = 2048 (1.14
+// PFLOP/s; 29.3 with 160-row tiles); a large library bf16 product reaches 1.5
+// to 1.6.  A wave's 128 x 64 tile fills the 256 registers that vector
+// instructions can address, which rules out larger ones; the clock falls to
+// 2.1 GHz under it, and the matrix pipes are busy 51% of the cycles.  Waves in
+// two groups that convert and multiply in turn were no faster.
 template <int BM, int BN, int WM, int WN, int S, int EPL, bool SW>
 __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   constexpr int NW = WM * WN, THREADS = NW * kWave;
@@ -370,7 +373,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
 #pragma unroll
           for (int n = 0; n < NL; ++n) {
             b[n].load(st + (BM + (n * WN + wn) * 16) * kBK, o0, o1);
-            if (n == 1) __builtin_amdgcn_sched_barrier(0);
+            if (n == 1) __builtin_amdgcn_sched_barrier(0);   // no more than two tiles' bytes beside their operands
           }
           Raw ra;
           ra.load(st + wrow(0) * kBK, o0, o1);
@@ -445,7 +448,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
       for (int m = 0; m < MT; ++m) {
         const int f = ft * BM + wm * (BM / WM) + m * 16 + (lane >> 4) * 4;
         if (f < A.F)
-          *reinterpret_cast<uint2*>(yr + f) = uint2{pack_bf16(acc[m][n][0], acc[m][n][1]), pack_bf16(acc[m][n][2], acc[m][n][3])};
+          *reinterpret_cast<uint2*>(yr + f) =
+              uint2{pack_bf16(acc[m][n][0], acc[m][n][1]), pack_bf16(acc[m][n][2], acc[m][n][3])};
       }
     }
   } else {
@@ -523,7 +527,8 @@ int launch_tile(GemmArgs A, int64_t slots, int cus, hipStream_t st) {
   const int64_t tiles = (slots / A.bn + active) * nf;   // no fewer than the rows can need
   const int64_t grid = (tiles + 7) / 8 * 8;
   if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
-  const auto k = A.E <= 4 * kWave ? k_grouped_gemm<BM, BN, WM, WN, S, 4, SW> : k_grouped_gemm<BM, BN, WM, WN, S, 16, SW>;
+  const auto k = A.E <= 4 * kWave ? k_grouped_gemm<BM, BN, WM, WN, S, 4, SW>
+                                  : k_grouped_gemm<BM, BN, WM, WN, S, 16, SW>;
   return launch("k_grouped_gemm", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 

@@ -163,7 +163,7 @@ __device__ __forceinline__ v8bf w_part(const WBlock& b, int i) {
 template <int NT>
 __device__ __forceinline__ void layer_up_tiles(const LayerArgs& A, const LayerRoutes& R, int e, int first, int stride,
                                                float (*red)[2][NT * 16][17]) {
-  constexpr int kXBufs = NT == 1 ? 2 : 1;   // with more columns the tokens' blocks are loaded when needed
+  constexpr int kXBufs = NT <= 2 ? 2 : 1;   // with more columns the tokens' blocks are loaded when needed
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int KB = A.H / kScaleBlock, IB = A.I / kScaleBlock, tiles = A.I / 16;
   const uint8_t* wexp = A.w13_q + ((int64_t)e * 2 * A.I + (lane & 15)) * A.H + (lane >> 4) * 16;
@@ -501,16 +501,23 @@ int launch_layer_ll(const Dims& D, const uint16_t* x, const int* idx, const floa
   const LayerArgs A = {x, idx, w, w13_q, w13_s, w2_q, w2_s, out, flags, a, a + (int64_t)slots * I,
                        reinterpret_cast<float*>(b + L.part), reinterpret_cast<int*>(b), splits,
                        tokens, slots, D.k, D.E, D.H, I};
-  const bool wide = slots > 8 * active;   // many tokens an expert: more columns a pass over the weights
+  // Columns of a pass over the weights, in tiles of 16 members, by the members
+  // that an active expert has on average (at most 64, H = 7168, I = 2048, 8
+  // experts).  Up: 16 members 91 us with one tile, 81 with two, 112 with four;
+  // 8 members 58, 71, 100; 64 members 230, 181, 157.  Down: 16 members 85, 93,
+  // 99; 64 members 191, 172, 156.
+  const int members = slots / active;
+  const auto up = members > 32 ? k_layer_up<4> : members > 12 ? k_layer_up<2> : k_layer_up<1>;
+  const auto down = members > 32 ? k_layer_down<4> : k_layer_down<1>;
   // Tiles of one expert that a workgroup takes one after the other: about 256
   // KiB of weights, as long as that leaves 2048 workgroups.
   const int tiles = I / 16;
   const int64_t most = (int64_t)tiles * active / 2048, want = (256 << 10) / (32 * D.H);
   const int turns = (int)(want < 1 || most < 1 ? 1 : want < most ? want : most);
-  int rc = launch("k_layer_up", wide ? k_layer_up<4> : k_layer_up<1>, dim3((tiles + turns - 1) / turns, active),
+  int rc = launch("k_layer_up", up, dim3((tiles + turns - 1) / turns, active),
                   dim3(kLayerUpWaves * kWave), 0, st, A);
   if (rc) return rc;
-  return launch("k_layer_down", wide ? k_layer_down<4> : k_layer_down<1>, dim3(D.H / kLayerDownRows, splits),
+  return launch("k_layer_down", down, dim3(D.H / kLayerDownRows, splits),
                 dim3(kLayerDownWaves * kWave), (size_t)kLayerDownWaves * tokens * kLayerDownRows * sizeof(float), st, A);
 }
 

@@ -262,7 +262,9 @@ def check_layer(out, N, T, H, k, x, idx, w, w13_q, w13_s, w2_q, w2_s):
     (64, 1, 256, 64, 1, 1152),
     (1, 64, 256, 1, 1, 640),
     (1, 3, 256, 1024, 64, 128),          # the most experts and slots a token
-    (1, 40, 128, 3, 3, 128),             # 40 members an expert: several column tiles
+    (1, 40, 128, 3, 3, 128),             # 40 members an expert: four column tiles at once
+    (1, 64, 384, 4, 1, 256),             # about 16: two tiles, with a second pass where there are more than 32
+    (1, 48, 256, 24, 8, 256),            # 16 of 24 experts a token
 ])
 def test_layer_shapes(N, T, H, E, k, I):  # noqa: E741
     log(f"layer N={N} T={T} H={H} E={E} k={k} I={I}")
