@@ -230,17 +230,18 @@ static_assert(2 * kXsChunk <= kWave, "one lane a weight scale");
 //
 // What bounds it on MI355X.  Plain form, 256 x 256, 2048 rows an expert: 9.5
 // ms for K = 2048 -> 7168 (1.62 PFLOP/s), 16.5 ms for 7168 -> 4096 (1.86);
-// a large library e4m3 product without block scales reaches 3.06.  The bound
-// is LDS: the waves read 192 KiB a step and the loads write 64, together the
-// 2048 cycles that the step's matrix instructions take; without the loads (a
-// timing copy) it is 2.5 PFLOP/s.  Weights loaded straight to registers,
-// prefetches into L2, smaller tiles with a third stage, and non-temporal
-// stores of y (11.4 ms) were slower.
+// a large library e4m3 product without block scales reaches 3.06.  No unit is
+// full: the matrix pipes are busy 36% of the cycles, LDS 16% (a counter that
+// may leave out the loads' writes), and waves wait for 37% of theirs.  A timing copy of an earlier step without the loads
+// of the K loop took 7.7 ms against 9.8 (12.3 against 17.1 for K = 7168), one
+// with a quarter of the scaled additions 9.3.  Weights loaded straight to
+// registers, prefetches into L2, smaller tiles with a third stage, and
+// non-temporal stores of y (11.4 ms) were slower.
 // SwiGLU form: 27.0 ms for 2048 rows an expert, K = 7168, I = 2048 (1.14
 // PFLOP/s; 29.3 with 160-row tiles); a large library bf16 product reaches 1.5
 // to 1.6.  A wave's 128 x 64 tile fills the 256 registers that vector
 // instructions can address, which rules out larger ones; the clock falls to
-// 2.1 GHz under it, and the matrix pipes are busy 51% of the cycles.  Waves in
+// 2.16 GHz under it, and the matrix pipes are busy 50% of the cycles.  Waves in
 // two groups that convert and multiply in turn were no faster.
 template <int BM, int BN, int WM, int WN, int S, int EPL, bool SW>
 __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {

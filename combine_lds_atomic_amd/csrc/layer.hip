@@ -393,7 +393,7 @@ __device__ __forceinline__ void layer_down_part(const LayerArgs& A, const LayerM
 // With several splits the sums go to memory and the tile's last workgroup (by
 // ticket) joins them in split order, so the result does not depend on timing.
 //
-// 29 us for one token of 8 experts (117 MB of weights), 260 us for 13 tokens
+// 31 us for one token of 8 experts (117 MB of weights), 261 us for 13 tokens
 // (1.26 GB, 4.8 TB/s).  With H = 2048 there are 64 tiles, and the splits count:
 // 64 tokens on 128 experts (0.53 GB) take 128 us, against 442 us with one
 // workgroup of 8 waves a tile.  The activation's two halves cost 12% (232 us
