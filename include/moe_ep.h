@@ -354,9 +354,11 @@ int moe_combine_recv_partial(const moe_shape *shape, const uint16_t *comb, const
  *   y         bf16 [N][T][H] out, n, or NULL: the tokens of a dispatch.
  *   y_q, y_s  fp8 e4m3fn [N][T][H] and fp32 [N][T][H/128] out, or both NULL:
  *             n quantised as dispatch quantises (scale = amax/448, IEEE
- *             division; a block of zeros has scale 0 and zero bytes), in the
- *             layout moe_grouped_gemm reads (a shared expert, say).  A block
- *             that holds an infinity or NaN gets that as its scale.
+ *             division; bytes rounded to nearest even, saturated at 448; a
+ *             block whose scale is 0, of zeros or below 3.2e-43, has zero
+ *             bytes), in the layout moe_grouped_gemm reads (a shared expert,
+ *             say).  A block that holds an infinity or NaN gets that as its
+ *             scale.
  * At least one of y and y_q.  res_out and y may be x or residual themselves
  * (same start), never a shifted overlap.  k, E and region_rows of the shape
  * do not matter here.

@@ -1,0 +1,84 @@
+"""The expert layer's operators on the GPU at the ends of the number range, on
+the tile and pass variants that few shapes reach, and under loads that gather
+on a few experts; against the float64 forms of tests/expert_ref.py."""
+import pytest
+import torch
+
+import combine_lds_atomic_amd as moe
+import expert_ref as X
+
+pytestmark = pytest.mark.gpu
+
+from gpu_harness import log  # noqa: E402
+
+TINY = 2.0 ** -149       # float32's smallest step
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def check_tiny_rows(q, s, v, dv):
+    """8-bit rows whose scales are near or below float32's smallest normal
+    number.  The scale amax / 448 is off by half of float32's smallest step
+    besides the value's own error, and 448 times that by at most
+    448 * 2^-150, which is also how far the saturated bytes of a block may
+    stay behind its largest values."""
+    b, db = v.reshape(v.shape[0], -1, 128), dv.reshape(v.shape[0], -1, 128)
+    amax, near = b.abs().amax(-1), db.amax(-1)
+    s = s.double()
+    off = (s - amax / 448.0).abs()
+    assert bool((off <= near / 448.0 + TINY / 2 + 4 * X.U * amax / 448.0).all()), f"scale off by {off.max().item()}"
+    assert not bool(((q & 0x7F) == 0x7F).any()), f"{int(((q & 0x7F) == 0x7F).sum())} bytes are NaN"
+    got = q.view(X.F8).double().reshape(b.shape) * s[..., None]
+    lim = X.E4M3_HALF * (b.abs() + db) + X.E4M3_SUB * 1.01 * s[..., None] + 448.0 * TINY / 2 + 3 * db
+    d = (got - b).abs()
+    assert bool((d <= lim).all()), f"{int((d > lim).sum())} bytes off, worst {(d / lim).max().item()}"
+
+
+# ------------------------------------------------------------------ subnormal scales
+
+def test_norm_subnormal_scales():
+    """Block maxima from about 1e-43 to 1e-39: the scales have one to a dozen
+    bits, and quotients reach 1.5 times 448."""
+    R, H = 48, 1280
+    log(f"norm R={R} H={H}, subnormal scales")
+    g = gen(91)
+    down = torch.arange(10, device="cuda")[None, :, None] * 1.4         # the first block sets the row's norm
+    x = (torch.randn((R, 10, 128), generator=g, device="cuda") * 2.0 ** -down).reshape(1, R, H).bfloat16()
+    gamma = torch.full((H,), 3 * 2.0 ** -133, device="cuda").bfloat16()
+    assert (gamma.double() == 3 * 2.0 ** -133).all()
+    sh = moe.shape(1, R, H, 1, 1)
+    q = torch.empty((1, R, H), dtype=torch.uint8, device="cuda")
+    s = torch.empty((1, R, H // 128), device="cuda")
+    moe.moe_rmsnorm_quant(sh, x, None, gamma, 1e-6, None, None, q, s)
+    _, n, rel = X.norm(x[0], None, gamma, 1e-6)
+    amax = n.abs().reshape(R, -1, 128).amax(-1)
+    assert float(amax.min()) < 8e-43 and float(amax.max()) > 1e-40      # the range the test is about
+    check_tiny_rows(q[0], s[0], n, n.abs() * rel + TINY)
+
+
+@pytest.mark.parametrize("E,T,I", [(1, 24, 256), (1, 200, 256), (64, 32768, 512)])   # narrow, middle and large tile
+def test_swiglu_subnormal_scales(E, T, I):  # noqa: E741
+    """The activation is quadratic in a small input's scale: block maxima from
+    3e-43 to 2e-41."""
+    log(f"swiglu E={E} T={T} I={I}, subnormal scales")
+    g = gen(92 + T)
+    K, n = 256, T // E
+    sh = moe.shape(1, T, 128, E, 1)
+    eo = (torch.arange(E + 1, device="cuda") * n).int()[None]
+    groups = [(e, e * n, n) for e in range(E)]
+    x_q, _ = X.quantise(torch.randn((T, K), generator=g, device="cuda"))
+    w_q, w_s = X.weights(E, 2 * I, K, g)
+    one = torch.ones((T, K // 128), device="cuda")
+    most = torch.empty(T, dtype=torch.float64, device="cuda")
+    for sl, h, _ in X.gemm(x_q, one, w_q, w_s, groups):
+        most[sl] = (h[:, :I] * h[:, I:]).abs().amax(1) / 2
+    want = torch.logspace(-42.5, -40.7, T, device="cuda", dtype=torch.float64)
+    x_s = (want / most).sqrt().float()[:, None].expand(T, K // 128).contiguous()
+    q, s = torch.empty((T, I), dtype=torch.uint8, device="cuda"), torch.empty((T, I // 128), device="cuda")
+    moe.moe_grouped_gemm_swiglu(sh, x_q, x_s, w_q, w_s, eo, K, I, q, s)
+    for sl, a, da in X.swiglu(x_q, x_s, w_q, w_s, groups):
+        check_tiny_rows(q[sl], s[sl], a, da + TINY)
