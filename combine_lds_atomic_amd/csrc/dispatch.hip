@@ -25,6 +25,7 @@
 #include <mutex>
 #include <tuple>
 
+#include "quant_dev.h"
 #include "route_dev.h"
 
 
@@ -38,20 +39,6 @@ constexpr int kOsWaves = kOsThreads / kWave;  // one-shot pack work items per wo
 constexpr int kPackWaves = 1;
 constexpr int kLlWaves = kThreads / kWave;    // single-launch packer waves per workgroup
 constexpr int kPackPasses = 4;                // passes whose loads a single-launch packer issues together
-
-// Four quotients x[i] / scale (IEEE division) packed as e4m3fn bytes,
-// little end first.  v_cvt_pk_fp8_f32 converts two floats to OCP e4m3fn
-// (round to nearest even, saturating) per instruction on gfx950; the
-// exhaustive sweep test checks its bytes against the oracle's encoder on
-// every bfloat16 pair x <= amax.
-__device__ __forceinline__ uint32_t quant4(const float* v, float scale) {
-  float q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = v[i] / scale;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-  return (uint32_t)w;
-}
 
 // This lane's 16 elements of each pass of the chunk starting at column c0
 // (zero beyond h1).
@@ -84,7 +71,7 @@ __device__ __forceinline__ v4u quant16(const v4u& a, const v4u& b, float& sc) {
   for (int i = 0; i < 16; ++i) am = max(am, (int)(__float_as_uint(v[i]) & 0x7FFFFFFFu));
   am = max8_lanes(am);                     // amax of the 128-element block
   const float amax = __uint_as_float((uint32_t)am);
-  const float scale = amax / 448.0f;       // IEEE division, round to nearest even
+  const float scale = block_scale(am);
   v4u q = {0, 0, 0, 0};
   if (amax != 0.0f) {
 #pragma unroll

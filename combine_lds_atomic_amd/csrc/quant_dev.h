@@ -1,4 +1,6 @@
-// Block-128 e4m3 quantisation shared by the kernels that write 8-bit rows.
+// Block-128 e4m3 quantisation, shared by the kernels that write 8-bit rows:
+// dispatch (from bfloat16 tokens), the norm and the SwiGLU product (from
+// float32).
 #pragma once
 
 #include "moe_internal.h"
@@ -13,14 +15,30 @@ namespace moe {
 // holds one gets that scale.
 __device__ __forceinline__ float block_scale(int amax_bits) { return __uint_as_float((uint32_t)amax_bits) / 448.0f; }
 
-// Four quotients v[i] / scale (IEEE division) of float32 values as e4m3fn
-// bytes, little end first, rounded to nearest even and saturated.  Zero bytes
-// where the scale is 0.
-//
-// v_cvt_pk_fp8_f32 rounds what is up to 464 to 448 and turns all above into
-// NaN.  Quotients pass 448 by a rounding where the scale is a normal number,
-// and by up to a half where it is a subnormal one of few bits: only those are
-// held to 448 (a select for every value took 2% of the norm's time).
+// Four quotients as e4m3fn bytes, little end first.  v_cvt_pk_fp8_f32 converts
+// two floats to OCP e4m3fn per instruction, rounded to nearest even; what is up
+// to 464 rounds to 448, and all above becomes NaN.
+__device__ __forceinline__ uint32_t fp8x4(const float (&q)[4]) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+  return (uint32_t)w;
+}
+
+// Four quotients v[i] / scale (IEEE division) of bfloat16 values, for a scale
+// above 0.  No block of bfloat16 values has a scale below 2.0e-43, whose
+// quotients are at most 450; the exhaustive sweep test checks the bytes against
+// the oracle's encoder on every bfloat16 pair x <= amax.
+__device__ __forceinline__ uint32_t quant4(const float* v, float scale) {
+  float q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = v[i] / scale;
+  return fp8x4(q);
+}
+
+// The same for float32 values, saturated, and zero bytes where the scale is 0.
+// Quotients pass 448 by a rounding where the scale is a normal number, and by
+// up to a half where it is a subnormal one of few bits: only those are held to
+// 448 (a select for every value took 2% of the norm's time).
 __device__ __forceinline__ uint32_t quant4_scaled(const float* v, float scale) {
   if (scale == 0.0f) return 0u;
   float q[4];
@@ -30,9 +48,7 @@ __device__ __forceinline__ uint32_t quant4_scaled(const float* v, float scale) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = fminf(fmaxf(q[i], -448.0f), 448.0f);
   }
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-  return (uint32_t)w;
+  return fp8x4(q);
 }
 
 __device__ __forceinline__ int abs_bits(float v) { return (int)(__float_as_uint(v) & 0x7FFFFFFFu); }

@@ -82,3 +82,35 @@ def test_swiglu_subnormal_scales(E, T, I):  # noqa: E741
     moe.moe_grouped_gemm_swiglu(sh, x_q, x_s, w_q, w_s, eo, K, I, q, s)
     for sl, a, da in X.swiglu(x_q, x_s, w_q, w_s, groups):
         check_tiny_rows(q[sl], s[sl], a, da + TINY)
+
+
+# ------------------------------------------------------------------ one quantiser
+
+def test_norm_rows_are_dispatchs_bytes():
+    """A row of ones has norm 1, so y is gamma itself; the norm's 8-bit rows
+    then hold the same values as dispatch's of y, and the same bytes."""
+    H, T = 32768, 1
+    log(f"norm against dispatch H={H}")
+    g = gen(93)
+    bits = [torch.randint(0, 1 << 16, (H,), generator=g, device="cuda")]                       # every exponent in a block
+    bits.append(torch.randint(0x3C00, 0x4200, (H,), generator=g, device="cuda"))               # near 1
+    bits[1] += torch.randint(0, 2, (H,), generator=g, device="cuda") << 15
+    bits.append(torch.randint(0, 0x100, (H,), generator=g, device="cuda"))                     # subnormal, many zeros
+    bits[2] *= torch.randint(0, 2, (H,), generator=g, device="cuda")
+    bits.append(torch.randint(1, 5, (H,), generator=g, device="cuda"))                         # the smallest numbers
+    bits.append((torch.randint(0, 2, (H,), generator=g, device="cuda") << 15) + torch.repeat_interleave(
+        torch.randint(0, 0x7F80, (H // 128,), generator=g, device="cuda"), 128))               # one magnitude a block
+    sh = moe.shape(1, T, H, 1, 1)
+    x = torch.ones((1, T, H), dtype=torch.bfloat16, device="cuda")
+    B = moe.allocate(sh, "cuda")
+    idx = torch.zeros((1, T, 1), dtype=torch.int32, device="cuda")
+    for b in bits:
+        b = torch.where((b & 0x7F80) == 0x7F80, b & 0xBFFF, b)                                  # finite
+        gamma = torch.where(b >= 1 << 15, b - (1 << 16), b).to(torch.int16).view(torch.bfloat16)
+        y = torch.empty_like(x)
+        q, s = torch.empty((1, T, H), dtype=torch.uint8, device="cuda"), torch.empty((1, T, H // 128), device="cuda")
+        moe.moe_rmsnorm_quant(sh, x, None, gamma, 1e-12, None, y, q, s)
+        assert torch.equal(y.view(torch.int16).flatten(), gamma.view(torch.int16))
+        moe.moe_dispatch_direct(sh, y, idx, B.x_q, B.x_s, B.send_pos, B.exp_off, B.row_src, B.ws)
+        assert torch.equal(B.x_q.flatten()[:H].view(torch.uint8), q.flatten())
+        assert torch.equal(B.x_s.flatten()[:H // 128], s.flatten())
