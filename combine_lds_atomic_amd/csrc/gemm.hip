@@ -131,18 +131,23 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& A, int nf) {
 // into LDS: lane i's bytes land at dst + 16*i (dst wave-uniform).  There is no
 // register result, and the wait is wait_and_barrier's: with the builtin the
 // compiler waits for all of these loads before the next LDS read that follows
-// one, however far apart their buffers are.
+// one, however far apart their buffers are.  The bytes arrive after the
+// statement: no wave reads them before the wait_and_barrier that follows it,
+// and none overwrites what another still reads, since every stage's and scale
+// buffer's last reader passed a barrier before its next load is issued.
 __device__ __forceinline__ uint32_t lds_address(const void* dst) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)dst);
 }
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t off, void* dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_address(dst)), "v"(off),
-               "s"(base));
+               "s"(base)
+               : "m0", "memory");
 }
 // The same with 4 bytes a lane.
 __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, void* dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds_address(dst)), "v"(off),
-               "s"(base));
+               "s"(base)
+               : "m0", "memory");
 }
 
 // Wait until at most `Left` of this wave's LDS loads are on their way and all
