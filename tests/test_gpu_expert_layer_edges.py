@@ -114,3 +114,36 @@ def test_norm_rows_are_dispatchs_bytes():
         moe.moe_dispatch_direct(sh, y, idx, B.x_q, B.x_s, B.send_pos, B.exp_off, B.row_src, B.ws)
         assert torch.equal(B.x_q.flatten()[:H].view(torch.uint8), q.flatten())
         assert torch.equal(B.x_s.flatten()[:H // 128], s.flatten())
+
+
+# ------------------------------------------------------------------ sums of the plain product
+
+@pytest.mark.parametrize("E,T,F", [(1, 9, 144), (1, 130, 144), (8, 16384, 4096)])   # narrow, middle and large tile
+def test_product_with_outliers_that_cancel(E, T, F):
+    """Two columns whose products are 448 * 448 and its negative, in different
+    groups of eight columns: what the e4m3 matrix instruction drops of their
+    neighbours is within the stated bound, and the other groups' products
+    arrive as if there were no outlier."""
+    log(f"product with outliers E={E} T={T} F={F}")
+    g = gen(95 + T)
+    K, n = 512, T // E
+    f8 = lambda *s: (torch.randn(s, generator=g, device="cuda") * 0.5).to(X.F8).view(torch.uint8)  # noqa: E731
+    x_q, w_q = f8(T, K), f8(E, F, K)
+    x_s = torch.ones((T, K // 128), device="cuda")
+    w_s = torch.ones((E, -(-F // 128), K // 128), device="cuda")
+    plus, minus = 131, 203                        # columns of the second block, of its first and tenth group
+    x_q[:, [plus, minus]] = 0x7E                  # 448
+    w_q[:, :, plus], w_q[:, :, minus] = 0x7E, 0xFE
+    eo = (torch.arange(E + 1, device="cuda") * n).int()[None]
+    y = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm(moe.shape(1, T, 128, E, 1), x_q, x_s, w_q, w_s, eo, K, F, y)
+    for e in range(E):
+        rows, feats = slice(e * n, e * n + min(n, 130)), slice(F - 144, F)
+        xv, wv = X.values(x_q[rows], x_s[rows]), X.values(w_q[e], w_s[e], 128)[feats]
+        # the outliers' own sum is exact in float32, so the sums round what is left: the groups' sums on
+        # 2^-23 of the 2^18 that passes through, then the blocks
+        ref = xv @ wv.T
+        d = X.e4m3_loss(xv, wv) + 16 * 2.0 ** (18 - 23)
+        lim = X.BF16_HALF * (ref.abs() + d) + d
+        off = (y[rows, feats].double() - ref).abs()
+        assert bool((off <= lim).all()), f"expert {e}: worst {(off / lim).max().item()}"
