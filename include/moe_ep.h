@@ -420,10 +420,13 @@ int moe_grouped_gemm_swiglu(const moe_shape *shape, const uint8_t *x_q, const fl
  * combined output in two launches, with no dispatched rows in between:
  *   out[s][t] = bf16_rne(sum_j topk_w[s][t][j] * W2[e] (silu(Wg[e] x) * (Wu[e] x))),
  *   e = topk_idx[s][t][j], x = tokens[s][t].
- * It reads each weight of a chosen expert once.  Unlike the path through
- * dispatch the tokens are not rounded to 8 bits: products are exact, sums in
- * float32, and the weighted activation between the two products is held in
- * 16 significand bits.
+ * Weights are read once for each pass of 16, 32 or 64 of an expert's tokens;
+ * the width is chosen for the average, N*T*k / min(N*T*k, E), so an expert
+ * that gathers more than that many tokens is read several times.  Unlike the
+ * path through dispatch the tokens are not rounded to 8 bits: products are
+ * exact, sums in float32, and the weighted activation between the two products
+ * is rounded to 16 significand bits (2^-17 of each value at most, beside the
+ * 2^-9 of the output's own rounding).
  *   shape     N*T at most 64, else MOE_EINVAL; region_rows does not matter.
  *   tokens    bf16 [N][T][H], 16-B aligned.
  *   topk_idx, topk_w  int32, fp32 [N][T][k].  A slot with an id outside
