@@ -425,8 +425,8 @@ int moe_grouped_gemm_swiglu(const moe_shape *shape, const uint8_t *x_q, const fl
  * that gathers more than that many tokens is read several times.  Unlike the
  * path through dispatch the tokens are not rounded to 8 bits: products are
  * exact, sums in float32, and the weighted activation between the two products
- * is rounded to 16 significand bits (2^-17 of each value at most, beside the
- * 2^-9 of the output's own rounding).
+ * is rounded to 16 significand bits (2^-16 of each value at most, beside the
+ * 2^-8 of the output's own rounding).
  *   shape     N*T at most 64, else MOE_EINVAL; region_rows does not matter.
  *   tokens    bf16 [N][T][H], 16-B aligned.
  *   topk_idx, topk_w  int32, fp32 [N][T][k].  A slot with an id outside
