@@ -10,6 +10,8 @@ import expert_ref as X
 pytestmark = pytest.mark.gpu
 
 from gpu_harness import log  # noqa: E402
+from test_gpu_expert_layer import (CHAIN, check_layer, layer_inputs, make_groups, run_chain, run_gemm,  # noqa: E402
+                                   run_layer, uneven)
 
 TINY = 2.0 ** -149       # float32's smallest step
 
@@ -36,6 +38,20 @@ def check_tiny_rows(q, s, v, dv):
     lim = X.E4M3_HALF * (b.abs() + db) + X.E4M3_SUB * 1.01 * s[..., None] + 448.0 * TINY / 2 + 3 * db
     d = (got - b).abs()
     assert bool((d <= lim).all()), f"{int((d > lim).sum())} bytes off, worst {(d / lim).max().item()}"
+
+
+@pytest.fixture(autouse=True)
+def no_nan_bytes(monkeypatch):
+    """A NaN byte beside a finite scale passes a comparison that asks whether
+    the difference is above a limit; here every 8-bit row is also looked at
+    for such bytes."""
+    check = X.check_quantised
+
+    def strict(q, s, v, dv, what=""):
+        nan = ((q & 0x7F) == 0x7F).reshape(*s.shape, 128) & s.isfinite()[..., None]
+        assert not bool(nan.any()), f"{what}: {int(nan.sum())} bytes are NaN"
+        check(q, s, v, dv, what)
+    monkeypatch.setattr(X, "check_quantised", strict)
 
 
 # ------------------------------------------------------------------ subnormal scales
@@ -147,3 +163,182 @@ def test_product_with_outliers_that_cancel(E, T, F):
         lim = X.BF16_HALF * (ref.abs() + d) + d
         off = (y[rows, feats].double() - ref).abs()
         assert bool((off <= lim).all()), f"expert {e}: worst {(off / lim).max().item()}"
+
+
+# ------------------------------------------------------------------ tile variants
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N,E,T,k,K,F", [
+    (4, 384, 4096, 4, 384, 256),        # more than 256 experts, 170 rows on average, uneven: the middle tile
+    (2, 300, 375, 20, 1152, 128),       # 50 on average, an expert count that no lane count divides
+    (1, 257, 100, 64, 256, 384),        # 24 on average: the narrow tile's upper end
+])
+def test_products_of_many_uneven_experts(swiglu, N, E, T, k, K, F):
+    log(f"gemm swiglu={swiglu} N={N} E={E} T={T} k={k} K={K} F={F}")
+    counts = uneven(E, N * T * k, T, zero_every=5)
+    assert max(counts) > 3 * N * T * k // E and min(counts) == 0
+    run_gemm(N, E, counts, K, F, T, k, swiglu=swiglu, seed=E)
+
+
+@pytest.mark.parametrize("N,E,T,k,K,F", [(1, 1, 1, 1, 128, 128), (2, 8, 9, 2, 384, 256), (4, 16, 100, 4, 1024, 384),
+                                         (2, 8, 2000, 2, 384, 4096), (4, 512, 19200, 2, 128, 256)])
+def test_swiglu_bytes_are_numbers(N, E, T, k, K, F):
+    """Each tile variant once more, with the look for NaN bytes."""
+    log(f"swiglu bytes N={N} E={E} T={T} k={k} K={K} F={F}")
+    run_gemm(N, E, uneven(E, N * T * k, T), K, F, T, k, swiglu=True, seed=K + 1)
+
+
+# ------------------------------------------------------------------ infinities
+
+def test_product_past_the_largest_numbers():
+    """Sums beyond bf16's and float32's range become infinities of their sign,
+    others of the row stay what they are, and so do the other rows."""
+    g = gen(96)
+    K, F, T = 128, 256, 5
+    log("product past the largest numbers")
+    x_q, x_s = X.quantise(torch.randn((T, K), generator=g, device="cuda"))
+    w_q, w_s = X.weights(1, F, K, g)
+    x_s[2] *= 2.5e38
+    x_s[3] = float("inf")
+    eo = make_groups(1, 1, [T])
+    y = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm(moe.shape(1, T, 128, 1, 1), x_q, x_s, w_q, w_s, eo, K, F, y)
+    for sl, r, d in X.gemm(x_q, x_s, w_q, w_s, [(0, 0, 2), (0, 4, 1)]):
+        assert bool(((y[sl].double() - r).abs() <= X.BF16_HALF * (r.abs() + d) + d).all())
+    xv, wv = X.values(x_q[2:3], x_s[2:3]), X.values(w_q[0], w_s[0], 128)
+    r = (xv @ wv.T)[0]
+    d = X.e4m3_loss(xv, wv)[0] + r.abs() * 4 * X.U
+    top = float(torch.finfo(torch.bfloat16).max) * (1 + 2.0 ** -9)      # from here on bf16 rounds to infinity
+    over, under = r.abs() - d > top, r.abs() + d < top
+    assert int(over.sum()) > 10 and int(under.sum()) > 100 and int((~(over | under)).sum()) < 10
+    got = y[2].double()
+    assert bool((got[over] == torch.sign(r[over]) * float("inf")).all())
+    assert bool(((got - r).abs() <= X.BF16_HALF * (r.abs() + d) + d)[under].all())
+    assert not bool(y[3].isfinite().any())
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_swiglu_past_the_largest_numbers(T):
+    """An activation beyond float32's range makes its block's scale infinite and
+    its byte NaN; an infinite gate or up makes the block infinite or NaN; the
+    other rows are what they were."""
+    g = gen(97)
+    K, I = 128, 256  # noqa: E741
+    log(f"swiglu past the largest numbers T={T}")
+    sh, eo = moe.shape(1, T, 128, 1, 1), make_groups(1, 1, [T])
+    x_q, x_s = X.quantise(torch.randn((T, K), generator=g, device="cuda"))
+    w_q, w_s = X.weights(1, 2 * I, K, g)
+
+    def go(x_s, w_s):
+        q, s = torch.empty((T, I), dtype=torch.uint8, device="cuda"), torch.empty((T, I // 128), device="cuda")
+        moe.moe_grouped_gemm_swiglu(sh, x_q, x_s, w_q, w_s, eo, K, I, q, s)
+        return q, s
+    q0, s0 = go(x_s, w_s)
+    big = x_s.clone()
+    big[2] *= 1e30                       # gate and up about 1e30, their product 1e60 where the gate is positive
+    big[3] = float("inf")                # every gate and up infinite
+    q, s = go(big, w_s)
+    keep = [t for t in range(T) if t not in (2, 3)]
+    assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
+    h = (X.values(x_q[2:3], big[2:3]) @ X.values(w_q[0], w_s[0], 128).T)[0]
+    gate, up = h[:I], h[I:]
+    assert float(gate.abs().min()) > 1e26 and float(up.abs().min()) > 1e26      # none is near zero
+    assert bool((s[2] == float("inf")).all())
+    assert bool((((q[2] & 0x7F) == 0x7F) == (gate > 0)).all()) and bool(((q[2] & 0x7F)[gate < 0] == 0).all())
+    assert not bool(s[3].isfinite().any())
+    for half in (0, 1):                  # an infinite scale of one block of gate, or of up, weights
+        bad = w_s.clone()
+        bad[0, half * (I // 128)] = float("inf")
+        q, s = go(x_s, bad)
+        assert not bool(s[:, 0].isfinite().any())
+        assert torch.equal(q[:, 128:], q0[:, 128:]) and torch.equal(s[:, 1:], s0[:, 1:])
+
+
+# ------------------------------------------------------------------ few-token layer under uneven loads
+
+def check_load(N, T, H, E, k, I, gather, seed):  # noqa: E741
+    """`gather`: (tokens, experts) that the first so many tokens choose alike."""
+    log(f"layer N={N} T={T} H={H} E={E} k={k} I={I} gather={gather}")
+    a = list(layer_inputs(N, T, H, E, k, I, seed=seed))
+    if gather:
+        n, chosen = gather
+        a[1].view(-1, k)[:n, :len(chosen)] = torch.tensor(chosen, dtype=torch.int32, device="cuda")
+    out, flags = run_layer(N, T, H, E, k, I, *a)
+    assert flags == 0
+    check_layer(out, N, T, H, k, *a)
+    again, _ = run_layer(N, T, H, E, k, I, *a)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("N,T,H,E,k,I,gather", [
+    (1, 64, 1024, 32, 8, 2048, None),                        # 16 members: two column tiles, two weight tiles a workgroup
+    (4, 16, 1152, 32, 8, 2048, (64, [5])),                   # ... one expert with all 64: a second pass over both
+    (1, 64, 640, 32, 20, 2048, None),                        # 40 members: four column tiles, two weight tiles
+    (1, 64, 384, 32, 24, 4096, (60, [31, 0, 7])),            # ... with four weight tiles, three experts nearly full
+    (8, 8, 512, 256, 8, 2048, (64, [0, 9, 99, 100, 128, 200, 254, 255])),   # all on 8 of 256: four passes of one tile
+    (1, 50, 256, 256, 4, 1024, (49, [17])),                  # 49 members of one tile: the last pass has one
+    (2, 16, 128, 64, 2, 2048, (32, [63])),                   # one block of columns: three of four waves have none
+])
+def test_layer_uneven_loads(N, T, H, E, k, I, gather):  # noqa: E741
+    check_load(N, T, H, E, k, I, gather, seed=H + E)
+
+
+def test_layer_calls_on_two_streams_and_one_workspace_for_two_shapes():
+    """Calls with workspaces of their own overlap freely; one workspace serves
+    calls of several shapes in order, captured and replayed."""
+    I = 384  # noqa: E741
+    shapes = [(1, 9, 384, 24, 3, I), (1, 33, 256, 4, 2, I)]
+    log(f"layer, two streams, shapes {shapes}")
+    cases = []
+    for i, c in enumerate(shapes):
+        a = layer_inputs(*c, seed=50 + i)
+        sh = moe.shape(*c[:5])
+        cases.append((c, a, sh, torch.empty_like(a[0]), torch.empty(1, dtype=torch.int32, device="cuda")))
+    want = [run_layer(*c, *a)[0] for c, a, *_ in cases]
+    need = [moe.moe_layer_ll_workspace_bytes(sh, I) for _, _, sh, *_ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    own = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in need]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (_, a, sh, out, fl), ws, st in zip(cases, own, streams):
+            moe.moe_layer_ll(sh, *a, I, out, fl, ws, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, _, out, _), w in zip(cases, want):
+        assert torch.equal(out, w)
+        out.zero_()
+    shared = torch.full((max(need),), 0xFF, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _, a, sh, out, fl in cases:
+            moe.moe_layer_ll(sh, *a, I, out, fl, shared)
+    for _ in range(3):
+        shared.fill_(0xFF)
+        for _, _, _, out, _ in cases:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, _, out, _), w in zip(cases, want):
+            assert torch.equal(out, w)
+
+
+# ------------------------------------------------------------------ together, first and last step
+
+@pytest.mark.parametrize("R", [0, 4 * 50 * 4])
+def test_chain_norm_and_combine(R):
+    """The first and last step of the layer that test_chain does not look at:
+    the norm's outputs, and the combine of exactly the down product's rows."""
+    log(f"chain R={R}: norm and combine")
+    c = run_chain(CHAIN, 256, R)
+    c["go"]()
+    B, N, T, H, k = c["B"], CHAIN.N, CHAIN.T, CHAIN.H, CHAIN.k
+    r, n, rel = X.norm(c["x"].view(-1, H), c["res"].view(-1, H), c["gamma"], 1e-6)
+    X.check_bf16(c["res_out"].view(-1, H), r, r.abs() * X.U)
+    X.check_bf16(c["y"].view(-1, H), n, n.abs() * rel)
+    X.check_quantised(c["y_q"], c["y_s"], n, n.abs() * rel)
+    comb = torch.zeros((N * T * k, H), dtype=torch.float64, device="cuda")
+    src = B.row_src.long()
+    comb[src[src >= 0]] = c["y_em"][src >= 0].double()
+    at = B.send_pos.view(N, T * k).long() + torch.arange(N, device="cuda")[:, None] * (T * k)
+    terms = comb[at.view(-1)].view(N * T, k, H) * c["w"].view(N * T, k, 1).double()
+    ref = terms.sum(1)
+    X.check_bf16(B.out.view(-1, H), ref, terms.abs().sum(1) * (2 * k * X.U))
