@@ -546,24 +546,39 @@ int launch_tile(GemmArgs A, int64_t slots, int cus, hipStream_t st) {
   return launch("k_grouped_gemm", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 
-// The tile goes by the rows that an active expert has on average:
-//   - above 256, and enough tiles: 256 rows.  2048 rows an expert: plain 9.7 ms
-//     against 10.9 with the middle tile, SwiGLU 27.0 against 29.3.
-//   - up to 256: the middle tile, 128 rows and three stages for the plain form
-//     (128 rows an expert, K = 2048 -> 7168: 1.03 ms against 1.05 with 160
-//     rows and two stages), 160 rows for SwiGLU (K = 7168, I = 2048: 2.32 ms
-//     against 2.65 with 128 rows, which half of the experts exceed, and 2.51
-//     with 256).
-//   - up to 24: 32 rows in workgroups of 4 waves, two on a compute unit; the
-//     weights' stream is the bound (5 rows an expert, K = 2048: plain 99 us
-//     against 106, SwiGLU 188 against 216 for the best middle tile).
+// The tile goes by the rows that an active expert has on average, all that the
+// host knows of the load.  us of each tile, even load but where noted; plain
+// form K = 2048 -> 7168, SwiGLU K = 7168, I = 2048, 64 experts; "Zipf": 256
+// experts, a few with most of the rows.
+//   - narrow, 32 rows in workgroups of 4 waves, two on a compute unit: the
+//     weights' stream is the bound.  Middle, 128 rows and three stages for the
+//     plain form (128 rows an expert, 256 experts: 1.03 ms against 1.05 with
+//     160 rows and two stages), 160 rows for SwiGLU (2.32 ms against 2.65 with
+//     128 rows, which half of the experts exceed, and 2.51 with 256).
+//       plain            8    16    24    32   Zipf 8   16   32
+//       narrow         171   176   179   202      282  409  581
+//       middle         169   174   179   185      295  388  493
+//       (128 experts, 2048 -> 2048: 2 rows 87 against 95, 12 rows 103 against
+//       107, 16 rows 104 against 107, 24 rows 119 against 110.)
+//       SwiGLU           8    24    32    40    48    56    64   Zipf 16   32   64
+//       narrow         313   344   342   415   402-428 479  498       727 1159 1868
+//       middle         377   401   406   427   412-430 433  440       875 1209 1754
+//   - large, 256 rows, above 256 rows where there are enough tiles.
+//       plain          128   160   224   256   320   512  1024   Zipf 128  256  400
+//       middle         269   321   379   420   514   768  1371      1026 1751 2481
+//       large          269   291   338   406   481   681  1244      1106 1719 2371
+//       SwiGLU         128   160   224   256   288   320   512  1024   Zipf 160  256  400
+//       middle         620   778   953  1031  1188  1325  1980  3802      3315 4823 7063
+//       large          632   706   899  1074  1247  1267  1818  3403      3531 4815 7159
+//     From 144 to 224 rows an even load would gain from it and an uneven one
+//     lose as much, so those stay with the middle tile.
 template <bool SW>
 int launch_any(const GemmArgs& A, int64_t slots, int cus, hipStream_t st) {
-  constexpr int BF = SW ? 128 : 256;
+  constexpr int BF = SW ? 128 : 256, kNarrowRows = SW ? 48 : 12;
   const int64_t active = slots < A.E ? slots : A.E, avg = slots / active;
   const int64_t big = active * ((avg + 255) / 256) * ((A.F + BF - 1) / BF);   // tiles of 256 rows
   if (avg > 256 && big >= 2 * cus) return launch_tile<256, 256, 2, 4, 2, SW>(A, slots, cus, st);
-  if (avg > 24) return launch_tile<256, SW ? 160 : 128, 4, 2, SW ? 2 : 3, SW>(A, slots, cus, st);
+  if (avg > kNarrowRows) return launch_tile<256, SW ? 160 : 128, 4, 2, SW ? 2 : 3, SW>(A, slots, cus, st);
   return launch_tile<256, 32, 4, 1, 2, SW>(A, slots, cus, st);
 }
 

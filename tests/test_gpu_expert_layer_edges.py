@@ -171,7 +171,9 @@ def test_product_with_outliers_that_cancel(E, T, F):
 @pytest.mark.parametrize("N,E,T,k,K,F", [
     (4, 384, 4096, 4, 384, 256),        # more than 256 experts, 170 rows on average, uneven: the middle tile
     (2, 300, 375, 20, 1152, 128),       # 50 on average, an expert count that no lane count divides
-    (1, 257, 100, 64, 256, 384),        # 24 on average: the narrow tile's upper end
+    (1, 257, 100, 64, 256, 384),        # 24 on average: the plain form's middle, SwiGLU's narrow tile
+    (1, 260, 195, 64, 256, 128),        # 48 on average: SwiGLU's narrow tile at its upper end
+    (2, 100, 100, 6, 512, 384),         # 12 on average: the plain form's narrow tile at its upper end
 ])
 def test_products_of_many_uneven_experts(swiglu, N, E, T, k, K, F):
     log(f"gemm swiglu={swiglu} N={N} E={E} T={T} k={k} K={K} F={F}")
