@@ -33,7 +33,7 @@ int launch(const char* name, void (*k)(KArgs...), dim3 grid, dim3 block, size_t 
 }
 
 constexpr int kWave = 64;            // CDNA wavefront width
-constexpr int kWavesPerBlock = 4;    // 256-thread workgroups everywhere
+constexpr int kWavesPerBlock = 4;    // of the routing and row kernels; others state their own
 constexpr int kThreads = kWave * kWavesPerBlock;
 constexpr int kMaxN = 256;
 constexpr int kMaxE = 1024;

@@ -360,8 +360,8 @@ int moe_combine_recv_partial(const moe_shape *shape, const uint16_t *comb, const
  *             say).  A block that holds an infinity or NaN gets that as its
  *             scale.
  * At least one of y and y_q.  res_out and y may be x or residual themselves
- * (same start), never a shifted overlap.  k, E and region_rows of the shape
- * do not matter here.
+ * (same start), never a shifted overlap.  The shape must be a valid one, but
+ * its k, E and region_rows change nothing here.
  */
 int moe_rmsnorm_quant(const moe_shape *shape, const uint16_t *x, const uint16_t *residual, const uint16_t *gamma,
                       float eps, uint16_t *res_out, uint16_t *y, uint8_t *y_q, float *y_s, void *stream);
@@ -386,8 +386,9 @@ int moe_rmsnorm_quant(const moe_shape *shape, const uint16_t *x, const uint16_t 
  *   exp_off   int32 [N][E/N+1], from dispatch.  With packed regions rank d's
  *             rows follow rank d-1's.
  *   K, F      input and output features: K a multiple of 128, 128..32768; F a
- *             multiple of 16, 16..32768, else MOE_EINVAL.  The shape's H does
- *             not matter here, so one shape serves both products of a layer.
+ *             multiple of 16, 16..32768, else MOE_EINVAL.  The shape's H
+ *             must be valid but changes nothing here, so one shape serves
+ *             both products of a layer.
  *   y         bf16 [rows][F] out, 16-B aligned: y_em of the combine.
  * The output must not overlap an input.  A shape whose tiles do not fit one
  * launch (2^32 threads; far beyond what the arrays would fit) is MOE_ERANGE.
@@ -427,7 +428,8 @@ int moe_grouped_gemm_swiglu(const moe_shape *shape, const uint8_t *x_q, const fl
  * exact, sums in float32, and the weighted activation between the two products
  * is rounded to 16 significand bits (2^-16 of each value at most, beside the
  * 2^-8 of the output's own rounding).
- *   shape     N*T at most 64, else MOE_EINVAL; region_rows does not matter.
+ *   shape     N*T at most 64, else MOE_EINVAL; region_rows must be valid but
+ *             changes nothing.
  *   tokens    bf16 [N][T][H], 16-B aligned.
  *   topk_idx, topk_w  int32, fp32 [N][T][k].  A slot with an id outside
  *             [0, E) contributes nothing; an expert that a token names twice
