@@ -241,20 +241,21 @@ static_assert(2 * kXsChunk <= kWave, "one lane a weight scale");
 //     multiplied there, at half the instruction's rate and 1.5 to 2
 //     conversions per instruction (2e-7 against 64-bit sums).
 //
-// What bounds it on MI355X.  Plain form, 256 x 256, 2048 rows an expert: 9.5
-// ms for K = 2048 -> 7168 (1.62 PFLOP/s), 16.5 ms for 7168 -> 4096 (1.86);
-// a large library e4m3 product without block scales reaches 3.06.  No unit is
-// full: the matrix pipes are busy 36% of the cycles, LDS 16% (a counter that
-// may leave out the loads' writes), and waves wait for 37% of theirs.  A timing copy of an earlier step without the loads
-// of the K loop took 7.7 ms against 9.8 (12.3 against 17.1 for K = 7168), one
+// What bounds it on MI355X (ranges are over boxes and runs).  Plain form, 256 x
+// 256, 2048 rows an expert: 9.3 to 10.0 ms for K = 2048 -> 7168 (1.54 to 1.66
+// PFLOP/s), 16.5 to 17.4 ms for 7168 -> 4096 (1.77 to 1.86); a large library
+// e4m3 product without block scales reaches 3.06.  No unit is full: the matrix
+// pipes are busy 36% of the cycles, LDS 16% (a counter that may leave out the
+// loads' writes), and waves wait for 37% of theirs.  A timing copy of an
+// earlier step without the loads of the K loop took 7.7 ms against 9.8 (12.3 against 17.1 for K = 7168), one
 // with a quarter of the scaled additions 9.3.  Weights loaded straight to
 // registers, prefetches into L2, smaller tiles with a third stage, and
 // non-temporal stores of y (11.4 ms) were slower.
-// SwiGLU form: 27.0 ms for 2048 rows an expert, K = 7168, I = 2048 (1.14
-// PFLOP/s; 29.3 with 160-row tiles); a large library bf16 product reaches 1.5
-// to 1.6.  A wave's 128 x 64 tile fills the 256 registers that vector
+// SwiGLU form: 26.3 to 29.0 ms for 2048 rows an expert, K = 7168, I = 2048
+// (1.06 to 1.17 PFLOP/s; with 160-row tiles 29.3 where this took 27.0); a large
+// library bf16 product reaches 1.5 to 1.6.  A wave's 128 x 64 tile fills the 256 registers that vector
 // instructions can address, which rules out larger ones; the clock falls to
-// 2.16 GHz under it, and the matrix pipes are busy 50% of the cycles.  Waves in
+// 2.2 GHz under it, and the matrix pipes are busy 50% of the cycles.  Waves in
 // two groups that convert and multiply in turn were no faster.
 template <int BM, int BN, int WM, int WN, int S, int EPL, bool SW>
 __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {

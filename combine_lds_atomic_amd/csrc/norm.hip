@@ -54,7 +54,7 @@ __device__ __forceinline__ void unpack8(const v4u& a, float* f) {
 // Bound by HBM: 4 H bytes in and 5 H + H/32 out per row.  Two units a thread
 // (448 threads at H = 7168) measured 679 us on 65536 rows, 6.25 TB/s, against
 // a plain copy's 6.6; one unit 815 us, four 677, a wave per row (14 units)
-// 790 (720 to 760 us for the first on other days).  On 4096 rows 53, 59, 56
+// 790 (709 to 760 us for the first on other days).  On 4096 rows 53, 59, 56
 // and 70 us.  Several rows a workgroup, one after the other with gamma kept
 // and the next row's loads in flight, were slower: 744 us for one row, 784
 // for four, 866 for sixteen, in one run.
