@@ -3,8 +3,8 @@ MI355X).  Argument marshalling only: every function forwards torch tensors'
 device pointers and the current HIP stream to the C ABI of
 ``include/moe_ep.h`` under the same name; all computation happens in the HIP
 kernels.  The expert layer's functions also check each tensor's type,
-contiguity, size and device first (TypeError, ValueError).  Importing this
-module fails loudly if the library is not built.
+contiguity, size and device, and the stream's device, first (TypeError,
+ValueError).  Importing this module fails loudly if the library is not built.
 """
 from __future__ import annotations
 
@@ -133,6 +133,8 @@ def _device() -> int:
 
 def _raw_stream(stream, dev):
     if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"stream is on device {stream.device_index}, not on the current GPU")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
 

@@ -92,6 +92,18 @@ def test_layer_workspace_holds_the_activation():
         assert b >= 4 * T * k * I and b % 256 == 0
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    """The kernels are launched for the current device; its streams only."""
+    class Stream:
+        cuda_stream = 0x1234
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+    assert moe._raw_stream(Stream(1), 1) == 0x1234
+    with pytest.raises(ValueError, match="stream is on device 1, not on the current GPU"):
+        moe._raw_stream(Stream(1), 0)
+
+
 def test_binding_checks_tensors():
     """Type, contiguity, size and device are checked before a pointer is taken."""
     x = torch.zeros((2, 8, 256), dtype=torch.bfloat16)
