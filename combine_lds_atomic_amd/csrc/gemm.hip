@@ -241,22 +241,22 @@ static_assert(2 * kXsChunk <= kWave, "one lane a weight scale");
 //     multiplied there, at half the instruction's rate and 1.5 to 2
 //     conversions per instruction (2e-7 against 64-bit sums).
 //
-// What bounds it on MI355X (ranges are over boxes and runs).  Plain form, 256 x
-// 256, 2048 rows an expert: 9.3 to 10.0 ms for K = 2048 -> 7168 (1.54 to 1.66
-// PFLOP/s), 16.5 to 17.4 ms for 7168 -> 4096 (1.77 to 1.86); a large library
-// e4m3 product without block scales reaches 3.06.  No unit is full: the matrix
-// pipes are busy 36% of the cycles, LDS 16% (a counter that may leave out the
-// loads' writes), and waves wait for 37% of theirs.  A timing copy of an
-// earlier step without the loads of the K loop took 7.7 ms against 9.8 (12.3 against 17.1 for K = 7168), one
-// with a quarter of the scaled additions 9.3.  Weights loaded straight to
-// registers, prefetches into L2, smaller tiles with a third stage, and
-// non-temporal stores of y (11.4 ms) were slower.
+// What bounds it on MI355X (ranges are over machines and runs).  Plain form,
+// 256 x 256, 2048 rows an expert: 9.3 to 10.0 ms for K = 2048 -> 7168 (1.54 to
+// 1.66 PFLOP/s), 16.5 to 17.4 ms for 7168 -> 4096 (1.77 to 1.86); a large
+// library e4m3 product without block scales reaches 3.06.  No unit is full: the
+// matrix pipes are busy 36% of the cycles, LDS 16% (a counter that may leave out
+// the loads' writes), and waves wait for 37% of theirs.  A timing copy of an
+// earlier step without the loads of the K loop took 7.7 ms against 9.8 (12.3
+// against 17.1 for K = 7168), one with a quarter of the scaled additions 9.3.
+// Weights loaded straight to registers, prefetches into L2, smaller tiles with a
+// third stage, and non-temporal stores of y (11.4 ms) were slower.
 // SwiGLU form: 26.3 to 29.0 ms for 2048 rows an expert, K = 7168, I = 2048
 // (1.06 to 1.17 PFLOP/s; with 160-row tiles 29.3 where this took 27.0); a large
-// library bf16 product reaches 1.5 to 1.6.  A wave's 128 x 64 tile fills the 256 registers that vector
-// instructions can address, which rules out larger ones; the clock falls to
-// 2.2 GHz under it, and the matrix pipes are busy 50% of the cycles.  Waves in
-// two groups that convert and multiply in turn were no faster.
+// library bf16 product reaches 1.5 to 1.6.  A wave's 128 x 64 tile fills the 256
+// registers that vector instructions can address, which rules out larger ones;
+// the clock falls to 2.2 GHz under it, and the matrix pipes are busy 50% of the
+// cycles.  Waves in two groups that convert and multiply in turn were no faster.
 template <int BM, int BN, int WM, int WN, int S, int EPL, bool SW>
 __global__ __launch_bounds__(WM* WN* kWave) void k_grouped_gemm(GemmArgs A) {
   constexpr int NW = WM * WN, THREADS = NW * kWave;
@@ -562,8 +562,8 @@ int launch_tile(GemmArgs A, int64_t slots, int cus, hipStream_t st) {
 //       (128 experts, 2048 -> 2048: 2 rows 87 against 95, 12 rows 103 against
 //       107, 16 rows 104 against 107, 24 rows 119 against 110.)
 //       SwiGLU           8    24    32    40    48    56    64   Zipf 16   32   64
-//       narrow         313   344   342   415   402-428 479  498       727 1159 1868
-//       middle         377   401   406   427   412-430 433  440       875 1209 1754
+//       narrow         313   344   342   415   428   479   498       727 1159 1868
+//       middle         377   401   406   427   430   433   440       875 1209 1754
 //   - large, 256 rows, above 256 rows where there are enough tiles.
 //       plain          128   160   224   256   320   512  1024   Zipf 128  256  400
 //       middle         269   321   379   420   514   768  1371      1026 1751 2481
