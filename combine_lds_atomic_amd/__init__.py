@@ -19,6 +19,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_ep.h")
 
 MOE_OK = 0
 ERRORS = {-1: "MOE_EINVAL", -2: "MOE_ENULL", -3: "MOE_EALIGN", -4: "MOE_ERANGE", -5: "MOE_EHIP"}
+WGRAD_F32, WGRAD_ADD = 1, 2
 FLAG_BADID, FLAG_OVERFLOW, FLAG_BOUND, FLAG_TIMEOUT = 1, 2, 4, 8
 
 
@@ -88,6 +89,15 @@ _SIG = {
     "moe_grouped_gemm_swiglu": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]),
     "moe_layer_ll_workspace_bytes": (ctypes.c_int64, [_S, ctypes.c_int32]),
     "moe_layer_ll": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P]),
+    "moe_ffn_up": (ctypes.c_int, [_S, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]),
+    "moe_grouped_gemm_bf16": (ctypes.c_int, [_S, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "moe_ffn_up_grad": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]),
+    "moe_grouped_wgrad": (ctypes.c_int, [_S, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_int32, _P]),
+    "moe_combine_grad": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_block_norm": (ctypes.c_int, [_S, _P, _P, _P, _P, ctypes.c_float, _P, ctypes.c_float, _P, _P, _P]),
+    "moe_block_norm_grad_workspace_bytes": (ctypes.c_int64, [_S]),
+    "moe_block_norm_grad": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, ctypes.c_float, _P, _P, _P,
+                                           _P, _P, _P, _P]),
     "moe_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_layout_export": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _P]),
 }
@@ -288,6 +298,94 @@ def moe_layer_ll(sh, tokens, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, I, out,
         _arg(f, "w2_q", w2_q, _F8, wq, dev), _arg(f, "w2_s", w2_s, _F32, wsc, dev), I,
         _arg(f, "out", out, _BF16, n * H, dev), _arg(f, "flags", flags, (torch.int32, torch.uint32), 1, dev),
         _arg(f, "ws", ws, (torch.uint8,), need, dev), _raw_stream(stream, dev)))
+
+
+def moe_ffn_up(sh, x, w13, exp_off, K, I, a, h_q, h_s, stream=None):  # noqa: E741
+    f, dev = "moe_ffn_up", _device()
+    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    _check(f, lib.moe_ffn_up(
+        ctypes.byref(sh), _arg(f, "x", x, _BF16, rows * K, dev), _arg(f, "w13", w13, _BF16, E * 2 * I * K, dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, I, _arg(f, "a", a, _BF16, rows * I, dev),
+        _arg(f, "h_q", h_q, _F8, rows * 2 * I, dev, True), _arg(f, "h_s", h_s, _F32, rows * (2 * I // 128), dev, True),
+        _raw_stream(stream, dev)))
+
+
+def moe_grouped_gemm_bf16(sh, x, w, exp_off, K, F, w_t, y, stream=None):
+    f, dev = "moe_grouped_gemm_bf16", _device()
+    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    _check(f, lib.moe_grouped_gemm_bf16(
+        ctypes.byref(sh), _arg(f, "x", x, _BF16, rows * K, dev), _arg(f, "w", w, _BF16, E * F * K, dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, F, bool(w_t),
+        _arg(f, "y", y, _BF16, rows * F, dev), _raw_stream(stream, dev)))
+
+
+def moe_ffn_up_grad(sh, dy, w2, h_q, h_s, exp_off, K, I, dh, a, stream=None):  # noqa: E741
+    f, dev = "moe_ffn_up_grad", _device()
+    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    _check(f, lib.moe_ffn_up_grad(
+        ctypes.byref(sh), _arg(f, "dy", dy, _BF16, rows * K, dev), _arg(f, "w2", w2, _BF16, E * K * I, dev),
+        _arg(f, "h_q", h_q, _F8, rows * 2 * I, dev), _arg(f, "h_s", h_s, _F32, rows * (2 * I // 128), dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, I,
+        _arg(f, "dh", dh, _BF16, rows * 2 * I, dev), _arg(f, "a", a, _BF16, rows * I, dev, True),
+        _raw_stream(stream, dev)))
+
+
+def moe_grouped_wgrad(sh, d, x, exp_off, F, K, dw, add=False, stream=None):
+    """dw's type, bfloat16 or float32, says which of the two is written."""
+    f, dev = "moe_grouped_wgrad", _device()
+    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    out = _arg(f, "dw", dw, _BF16 + _F32, sh.E * F * K, dev)
+    _check(f, lib.moe_grouped_wgrad(
+        ctypes.byref(sh), _arg(f, "d", d, _BF16, rows * F, dev), _arg(f, "x", x, _BF16, rows * K, dev),
+        _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), F, K, out,
+        (WGRAD_F32 if dw is not None and dw.dtype == torch.float32 else 0) | (WGRAD_ADD if add else 0),
+        _raw_stream(stream, dev)))
+
+
+def moe_combine_grad(sh, dout, y_em, topk_idx, send_pos, topk_w, row_src, ws, dy_em, dtopk_w, stream=None):
+    f, dev = "moe_combine_grad", _device()
+    n, rows = sh.N * sh.T, moe_recv_rows(sh) if sh.T else 0
+    _check(f, lib.moe_combine_grad(
+        ctypes.byref(sh), _arg(f, "dout", dout, _BF16, n * sh.H, dev),
+        _arg(f, "y_em", y_em, _BF16, rows * sh.H, dev, True), _arg(f, "topk_idx", topk_idx, _I32, n * sh.k, dev),
+        _arg(f, "send_pos", send_pos, _I32, n * sh.k, dev), _arg(f, "topk_w", topk_w, _F32, n * sh.k, dev, True),
+        _arg(f, "row_src", row_src, _I32, rows, dev, True),
+        _arg(f, "ws", ws, (torch.uint8,), moe_workspace_bytes(sh), dev),
+        _arg(f, "dy_em", dy_em, _BF16, rows * sh.H, dev, True),
+        _arg(f, "dtopk_w", dtopk_w, _F32, n * sh.k, dev, True), _raw_stream(stream, dev)))
+
+
+def moe_block_norm(sh, x, residual, gamma_post, gate, alpha, gamma_next, eps, res_out, y, stream=None):
+    f, dev = "moe_block_norm", _device()
+    t = sh.N * sh.T
+    n, H = t * sh.H, sh.H if t else 0
+    _check(f, lib.moe_block_norm(
+        ctypes.byref(sh), _arg(f, "x", x, _BF16, n, dev), _arg(f, "residual", residual, _BF16, n, dev),
+        _arg(f, "gamma_post", gamma_post, _BF16, H, dev), _arg(f, "gate", gate, _F32, t, dev, True), alpha,
+        _arg(f, "gamma_next", gamma_next, _BF16, H, dev, True), eps, _arg(f, "res_out", res_out, _BF16, n, dev),
+        _arg(f, "y", y, _BF16, n, dev, True), _raw_stream(stream, dev)))
+
+
+def moe_block_norm_grad_workspace_bytes(sh: moe_shape) -> int:
+    r = lib.moe_block_norm_grad_workspace_bytes(ctypes.byref(sh))
+    _check("moe_block_norm_grad_workspace_bytes", r if r < 0 else 0)
+    return int(r)
+
+
+def moe_block_norm_grad(sh, dy, dres_out, x, residual, gamma_post, gate, alpha, gamma_next, eps, dx, dresidual, dgate,
+                        dgamma_post, dgamma_next, ws, stream=None):
+    f, dev = "moe_block_norm_grad", _device()
+    t, H = sh.N * sh.T, sh.H
+    n = t * H
+    _check(f, lib.moe_block_norm_grad(
+        ctypes.byref(sh), _arg(f, "dy", dy, _BF16, n, dev, True), _arg(f, "dres_out", dres_out, _BF16, n, dev, True),
+        _arg(f, "x", x, _BF16, n, dev), _arg(f, "residual", residual, _BF16, n, dev),
+        _arg(f, "gamma_post", gamma_post, _BF16, H, dev), _arg(f, "gate", gate, _F32, t, dev, True), alpha,
+        _arg(f, "gamma_next", gamma_next, _BF16, H, dev, True), eps, _arg(f, "dx", dx, _BF16, n, dev),
+        _arg(f, "dresidual", dresidual, _BF16, n, dev), _arg(f, "dgate", dgate, _F32, t, dev, True),
+        _arg(f, "dgamma_post", dgamma_post, _F32, H, dev),
+        _arg(f, "dgamma_next", dgamma_next, _F32, H, dev, True),
+        _arg(f, "ws", ws, (torch.uint8,), moe_block_norm_grad_workspace_bytes(sh), dev), _raw_stream(stream, dev)))
 
 
 def moe_status(ws, stream=None) -> int:

@@ -25,7 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_ep.so")
 STREAMS_LIB = os.path.join(PKG, "libmoe_streams.so")
-SOURCES = ["abi.hip", "layout.hip", "dispatch.hip", "combine.hip", "norm.hip", "gemm.hip", "layer.hip"]
+SOURCES = ["abi.hip", "layout.hip", "dispatch.hip", "combine.hip", "norm.hip", "gemm.hip", "layer.hip", "ffn.hip",
+           "blocknorm.hip"]
 STREAMS_SOURCES = ["streams.hip"]
 ARCH = "gfx950"
 

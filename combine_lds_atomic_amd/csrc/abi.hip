@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/moe_ep.h: argument checks,
 // workspace carving, grid sizing and launches on the caller's stream.
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "moe_internal.h"
@@ -198,6 +199,25 @@ int gemm_args(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t
     return MOE_EALIGN;
   return MOE_OK;
 }
+
+// Host checks that the bfloat16 products share: K summed features, `out`
+// output features in steps of `step`; `need` are the arrays, 16-byte aligned.
+int product_args(const Dims& D, int32_t K, int32_t most_k, int32_t out, int32_t most_out, int32_t step,
+                 const int32_t* exp_off, std::initializer_list<const void*> need) {
+  if (K < kScaleBlock || K > most_k || K % kScaleBlock) return MOE_EINVAL;
+  if (out < step || out > most_out || out % step) return MOE_EINVAL;
+  if (D.T == 0) return MOE_OK;   // no rows: empty arrays may be NULL
+  if (!exp_off) return MOE_ENULL;
+  for (const void* p : need)
+    if (!p) return MOE_ENULL;
+  if (!aligned(exp_off, 4)) return MOE_EALIGN;
+  for (const void* p : need)
+    if (!aligned(p, 16)) return MOE_EALIGN;
+  return MOE_OK;
+}
+
+// Host checks of the numbers that a block's norms take.
+bool norm_numbers(float alpha, float eps) { return eps > 0.0f && std::isfinite(eps) && std::isfinite(alpha); }
 
 // Host checks of the few-token layer's shape.
 int layer_dims(const moe_shape* shape, int32_t I, Dims* D) {
@@ -496,6 +516,120 @@ int moe_layer_ll(const moe_shape* shape, const uint16_t* tokens, const int32_t* 
     return MOE_EALIGN;
   return launch_layer_ll(D, tokens, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, I, out, flags, ws,
                          as_stream(stream));
+}
+
+int moe_ffn_up(const moe_shape* shape, const uint16_t* x, const uint16_t* w13, const int32_t* exp_off, int32_t K,
+               int32_t I, uint16_t* a, uint8_t* h_q, float* h_s, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  rc = product_args(D, K, kMaxH, I, kMaxH, kScaleBlock, exp_off, {x, w13, a});
+  if (rc) return rc;
+  if (!h_q != !h_s) return MOE_ENULL;
+  if (!aligned(h_q, 16) || !aligned(h_s, 4)) return MOE_EALIGN;
+  if (D.T == 0) return MOE_OK;
+  return launch_ffn_up(D, x, w13, exp_off, K, I, a, h_q, h_s, device_cus(), as_stream(stream));
+}
+
+int moe_grouped_gemm_bf16(const moe_shape* shape, const uint16_t* x, const uint16_t* w, const int32_t* exp_off,
+                          int32_t K, int32_t F, int32_t w_t, uint16_t* y, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (w_t != 0 && w_t != 1) return MOE_EINVAL;
+  rc = product_args(D, K, 2 * kMaxH, F, kMaxH, 16, exp_off, {x, w, y});
+  if (rc || D.T == 0) return rc;
+  return launch_grouped_gemm_bf16(D, x, w, exp_off, K, F, w_t, y, device_cus(), as_stream(stream));
+}
+
+int moe_ffn_up_grad(const moe_shape* shape, const uint16_t* dy, const uint16_t* w2, const uint8_t* h_q,
+                    const float* h_s, const int32_t* exp_off, int32_t K, int32_t I, uint16_t* dh, uint16_t* a,
+                    void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  rc = product_args(D, K, kMaxH, I, kMaxH, kScaleBlock, exp_off, {dy, w2, h_q, dh});
+  if (rc || D.T == 0) return rc;
+  if (!h_s) return MOE_ENULL;
+  if (!aligned(h_s, 4) || !aligned(a, 16)) return MOE_EALIGN;
+  return launch_ffn_up_grad(D, dy, w2, h_q, h_s, exp_off, K, I, dh, a, device_cus(), as_stream(stream));
+}
+
+int moe_grouped_wgrad(const moe_shape* shape, const uint16_t* d, const uint16_t* x, const int32_t* exp_off, int32_t F,
+                      int32_t K, void* dw, int32_t flags, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (flags & ~(MOE_WGRAD_F32 | MOE_WGRAD_ADD)) return MOE_EINVAL;
+  rc = product_args(D, kScaleBlock, kScaleBlock, F, 2 * kMaxH, 16, exp_off, {d, x});
+  if (rc) return rc;
+  if (K < 16 || K > kMaxH || K % 16) return MOE_EINVAL;
+  if (!dw) return MOE_ENULL;
+  if (!aligned(dw, 16)) return MOE_EALIGN;
+  return launch_grouped_wgrad(D, d, x, exp_off, F, K, dw, flags & MOE_WGRAD_F32, flags & MOE_WGRAD_ADD,
+                              as_stream(stream));
+}
+
+int moe_combine_grad(const moe_shape* shape, const uint16_t* dout, const uint16_t* y_em, const int32_t* topk_idx,
+                     const int32_t* send_pos, const float* topk_w, const int32_t* row_src, const void* ws,
+                     uint16_t* dy_em, float* dtopk_w, void* stream) {
+  Dims D;
+  int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (!ws) return MOE_ENULL;
+  if (!aligned(ws, kAlign)) return MOE_EALIGN;
+  if (D.T == 0) return MOE_OK;
+  if (!dout || !topk_idx || !send_pos || (!dy_em && !dtopk_w) || !y_em != !dtopk_w) return MOE_ENULL;
+  if (D.R && dy_em && !row_src) return MOE_ENULL;
+  if (!aligned(dout, 16) || !aligned(y_em, 16) || !aligned(dy_em, 16) || !aligned(topk_idx, 4) ||
+      !aligned(send_pos, 4) || !aligned(topk_w, 4) || !aligned(row_src, 4) || !aligned(dtopk_w, 4))
+    return MOE_EALIGN;
+  return launch_comb_grad(D, W_of(D, const_cast<void*>(ws)), dout, y_em, topk_idx, send_pos, topk_w, row_src, dy_em,
+                          dtopk_w, as_stream(stream));
+}
+
+int moe_block_norm(const moe_shape* shape, const uint16_t* x, const uint16_t* residual, const uint16_t* gamma_post,
+                   const float* gate, float alpha, const uint16_t* gamma_next, float eps, uint16_t* res_out,
+                   uint16_t* y, void* stream) {
+  Dims D;
+  const int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (!norm_numbers(alpha, eps)) return MOE_EINVAL;
+  if (!gamma_next != !y) return MOE_ENULL;
+  if (D.T == 0) return MOE_OK;
+  if (!x || !residual || !gamma_post || !res_out) return MOE_ENULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma_post, 16) || !aligned(gate, 4) ||
+      !aligned(gamma_next, 16) || !aligned(res_out, 16) || !aligned(y, 16))
+    return MOE_EALIGN;
+  return launch_block_norm(D, x, residual, gamma_post, gate, alpha, gamma_next, eps, res_out, y, as_stream(stream));
+}
+
+int64_t moe_block_norm_grad_workspace_bytes(const moe_shape* shape) {
+  Dims D;
+  const int rc = make_dims(shape, &D);
+  return rc ? rc : block_norm_grad_workspace(D);
+}
+
+int moe_block_norm_grad(const moe_shape* shape, const uint16_t* dy, const uint16_t* dres_out, const uint16_t* x,
+                        const uint16_t* residual, const uint16_t* gamma_post, const float* gate, float alpha,
+                        const uint16_t* gamma_next, float eps, uint16_t* dx, uint16_t* dresidual, float* dgate,
+                        float* dgamma_post, float* dgamma_next, void* ws, void* stream) {
+  Dims D;
+  const int rc = make_dims(shape, &D);
+  if (rc) return rc;
+  if (!norm_numbers(alpha, eps)) return MOE_EINVAL;
+  if (!gamma_post || !dgamma_post || !ws || !gamma_next != !dgamma_next) return MOE_ENULL;
+  if (!aligned(gamma_post, 16) || !aligned(gamma_next, 16) || !aligned(dgamma_post, 4) || !aligned(dgamma_next, 4) ||
+      !aligned(ws, kAlign))
+    return MOE_EALIGN;
+  if (D.T > 0) {
+    if (!x || !residual || !dx || !dresidual || (!dy && !dres_out) || !dy != !gamma_next) return MOE_ENULL;
+    if (!aligned(dy, 16) || !aligned(dres_out, 16) || !aligned(x, 16) || !aligned(residual, 16) || !aligned(gate, 4) ||
+        !aligned(dx, 16) || !aligned(dresidual, 16) || !aligned(dgate, 4))
+      return MOE_EALIGN;
+  }
+  return launch_block_norm_grad(D, dy, dres_out, x, residual, gamma_post, gate, alpha, gamma_next, eps, dx, dresidual,
+                                dgate, dgamma_post, dgamma_next, ws, as_stream(stream));
 }
 
 int moe_status(void* ws, void* stream, uint32_t* flags) {

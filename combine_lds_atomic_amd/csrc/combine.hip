@@ -23,6 +23,12 @@
 //                         tokens)
 //   k_comb_recv_partial_os  the receive side of it: float32 sum of a token's
 //                         group rows, bf16 out
+//   k_comb_grad           the gradients of the weighted average: every slot's
+//                         row gets w * dout, every weight <dout, y>
+//                         (k_comb_zero_holes: zeros for the rows that a
+//                         fixed-region overflow left without a token)
+#include <algorithm>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -538,6 +544,94 @@ __global__ __launch_bounds__(kPsThreads) void k_comb_send_partial(Dims D, Ws W, 
   }
 }
 
+// Gradients of the weighted average: for slot (s,t,j) with expert-major row p,
+//   dy[p] = bf16(w[s][t][j] * dout[s][t]),  dw[s][t][j] = <dout[s][t], y[p]>  (0 without a row).
+// One workgroup per token, wave w taking slots w, w + 4, ...; a lane takes the
+// 16-byte units lane, lane + 64, ... of a row, U of them at a time.  ONE: U
+// covers the row, so the wave reads dout once and keeps it.  y (and dw) or dy
+// may be null, or the same memory; without weights (w null) every weight is 1.
+template <int U, bool ONE>
+__global__ __launch_bounds__(kThreads) void k_comb_grad(Dims D, Ws W, const uint16_t* __restrict__ dout,
+                                                       const uint16_t* y, const int* __restrict__ idx,
+                                                       const int* __restrict__ send_pos,
+                                                       const float* __restrict__ topk_w, uint16_t* dy,
+                                                       float* __restrict__ dw) {
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n16 = D.H / 8;
+  for (int64_t tok = blockIdx.x; tok < (int64_t)D.N * D.T; tok += gridDim.x) {
+    const v4u* __restrict__ ds = reinterpret_cast<const v4u*>(dout) + tok * n16;
+    const int s = (int)(tok / D.T);
+    v4u d[U];
+    auto read = [&](const v4u* p, int c0, v4u(&v)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * kWave + lane;
+        v[u] = c < n16 ? ld16(p + c) : v4u{0, 0, 0, 0};
+      }
+    };
+    if constexpr (ONE) read(ds, 0, d);
+    for (int j = wave; j < D.k; j += kWavesPerBlock) {
+      const int64_t slot = tok * D.k + j;
+      const int row = em_row_of(D, W, s, idx[slot], send_pos[slot]);
+      float dot = 0.0f;
+      if (row >= 0) {
+        const float w = topk_w ? topk_w[slot] : 1.0f;
+        for (int c0 = 0; c0 < n16; c0 += U * kWave) {
+          if constexpr (!ONE) read(ds, c0, d);
+          if (y) {
+            v4u v[U];
+            read(reinterpret_cast<const v4u*>(y) + (int64_t)row * n16, c0, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                dot = __builtin_fmaf(bf16_lo(d[u][i]), bf16_lo(v[u][i]), dot);
+                dot = __builtin_fmaf(bf16_hi(d[u][i]), bf16_hi(v[u][i]), dot);
+              }
+          }
+          if (dy) {
+            v4u* o = reinterpret_cast<v4u*>(dy) + (int64_t)row * n16;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int c = c0 + u * kWave + lane;
+              v4u r;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                r[i] = f32_to_bf16_rne(w * bf16_lo(d[u][i])) | (f32_to_bf16_rne(w * bf16_hi(d[u][i])) << 16);
+              if (c < n16) st16(o + c, r);
+            }
+          }
+        }
+      }
+      if (dw) {
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) dot += __shfl_xor(dot, m);
+        if (lane == 0) dw[slot] = dot;
+      }
+    }
+  }
+}
+
+// After a fixed-region overflow: zeros in the expert-major rows that have no
+// token (row_src -1), so that sums over an expert's rows may take them.
+__global__ __launch_bounds__(kThreads) void k_comb_zero_holes(Dims D, Ws W, const int* __restrict__ row_src,
+                                                             uint16_t* __restrict__ dy) {
+  const int lane = threadIdx.x & (kWave - 1), n16 = D.H / 8;
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t r0 = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~(kWave - 1)); r0 < D.rows; r0 += step) {
+    const int64_t r = r0 + lane;
+    bool hole = false;
+    if (r < D.rows) {
+      const int d = (int)(r / D.R);
+      hole = r - (int64_t)d * D.R < W.vprefix[d + 1] - W.vprefix[d] && row_src[r] < 0;
+    }
+    for (uint64_t m = __ballot(hole); m; m &= m - 1) {
+      v4u* row = reinterpret_cast<v4u*>(dy) + (r0 + __builtin_ctzll(m)) * n16;
+      for (int c = lane; c < n16; c += kWave) st16(row + c, v4u{0, 0, 0, 0});
+    }
+  }
+}
+
 int launch_comb_send(const Dims& D, const Ws& W, const uint16_t* y, const int* row_src, uint16_t* comb, int cus,
                      hipStream_t st) {
   if (D.N * D.TK == 0) return MOE_OK;
@@ -559,6 +653,21 @@ int launch_comb_pull(const Dims& D, const Ws& W, const uint16_t* y, const int* i
   if (D.N * D.T == 0) return MOE_OK;
   return launch("k_comb_pull_os", k_comb_pull_os, dim3(os_grid((int64_t)D.N * D.T * (D.H / 8), kPullUnits * kCombThreads)),
                 dim3(kCombThreads), 0, st, D, W, y, idx, send_pos, w, out);
+}
+
+int launch_comb_grad(const Dims& D, const Ws& W, const uint16_t* dout, const uint16_t* y, const int* idx,
+                     const int* send_pos, const float* w, const int* row_src, uint16_t* dy, float* dw,
+                     hipStream_t st) {
+  const int64_t tokens = (int64_t)D.N * D.T;
+  if (tokens == 0) return MOE_OK;
+  const int per = (D.H / 8 + kWave - 1) / kWave;   // units of a lane
+  const auto k = per <= 2 ? k_comb_grad<2, true> : per <= 4 ? k_comb_grad<4, true> : per <= 8 ? k_comb_grad<8, true>
+                 : per <= 16 ? k_comb_grad<16, true> : k_comb_grad<16, false>;
+  const int rc = launch("k_comb_grad", k, dim3(os_grid(tokens, 1)), dim3(kThreads), 0, st, D, W, dout, y, idx,
+                        send_pos, w, dy, dw);
+  if (rc || !D.R || !dy) return rc;
+  return launch("k_comb_zero_holes", k_comb_zero_holes, dim3((uint32_t)std::min<int64_t>((D.rows + kThreads - 1) / kThreads, 4096)),
+                dim3(kThreads), 0, st, D, W, row_src, dy);
 }
 
 constexpr int64_t kPsMinTokens = 16384;   // tokens (N*T) from which the cooperative form is used

@@ -267,6 +267,24 @@ int launch_grouped_gemm(const Dims& D, const uint8_t* x_q, const float* x_s, con
 int launch_grouped_gemm_swiglu(const Dims& D, const uint8_t* x_q, const float* x_s, const uint8_t* w_q,
                                const float* w_s, const int* exp_off, int K, int I, uint8_t* a_q, float* a_s, int cus,
                                hipStream_t st);
+int launch_ffn_up(const Dims& D, const uint16_t* x, const uint16_t* w13, const int* exp_off, int K, int I, uint16_t* a,
+                  uint8_t* h_q, float* h_s, int cus, hipStream_t st);
+int launch_grouped_gemm_bf16(const Dims& D, const uint16_t* x, const uint16_t* w, const int* exp_off, int K, int F,
+                             bool w_t, uint16_t* y, int cus, hipStream_t st);
+int launch_ffn_up_grad(const Dims& D, const uint16_t* dy, const uint16_t* w2, const uint8_t* h_q, const float* h_s,
+                       const int* exp_off, int K, int I, uint16_t* dh, uint16_t* a, int cus, hipStream_t st);
+int launch_grouped_wgrad(const Dims& D, const uint16_t* d, const uint16_t* x, const int* exp_off, int F, int K,
+                         void* dw, bool f32, bool add, hipStream_t st);
+int launch_comb_grad(const Dims& D, const Ws& W, const uint16_t* dout, const uint16_t* y, const int* idx,
+                     const int* send_pos, const float* w, const int* row_src, uint16_t* dy, float* dw, hipStream_t st);
+int launch_block_norm(const Dims& D, const uint16_t* x, const uint16_t* residual, const uint16_t* gamma_post,
+                      const float* gate, float alpha, const uint16_t* gamma_next, float eps, uint16_t* res_out,
+                      uint16_t* y, hipStream_t st);
+int64_t block_norm_grad_workspace(const Dims& D);
+int launch_block_norm_grad(const Dims& D, const uint16_t* dy, const uint16_t* dres, const uint16_t* x,
+                           const uint16_t* residual, const uint16_t* gamma_post, const float* gate, float alpha,
+                           const uint16_t* gamma_next, float eps, uint16_t* dx, uint16_t* dresidual, float* dgate,
+                           float* dgamma_post, float* dgamma_next, void* ws, hipStream_t st);
 int64_t layer_ll_workspace(const Dims& D, int I);
 int launch_layer_ll(const Dims& D, const uint16_t* x, const int* idx, const float* w, const uint8_t* w13_q,
                     const float* w13_s, const uint8_t* w2_q, const float* w2_s, int I, uint16_t* out, uint32_t* flags,

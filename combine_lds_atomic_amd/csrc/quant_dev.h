@@ -74,4 +74,14 @@ __device__ __forceinline__ v8bf widen8(uint32_t a, uint32_t b) {
   return u.v;
 }
 
+// The i-th of four e4m3 values (a dword, little end first), exactly.
+__device__ __forceinline__ float fp8_value(uint32_t w, int i) {
+  switch (i) {   // the byte's number is part of the instruction
+    case 0: return __builtin_amdgcn_cvt_f32_fp8(w, 0);
+    case 1: return __builtin_amdgcn_cvt_f32_fp8(w, 1);
+    case 2: return __builtin_amdgcn_cvt_f32_fp8(w, 2);
+    default: return __builtin_amdgcn_cvt_f32_fp8(w, 3);
+  }
+}
+
 }  // namespace moe

@@ -450,6 +450,165 @@ int moe_layer_ll(const moe_shape *shape, const uint16_t *tokens, const int32_t *
                  const uint8_t *w13_q, const float *w13_s, const uint8_t *w2_q, const float *w2_s, int32_t I,
                  uint16_t *out, uint32_t *flags, void *ws, void *stream);
 
+/* ---------------------------------------------------------------- training
+ *
+ * What training the expert layer needs next to dispatch and combine: the
+ * experts' products in bfloat16, their gradients, the gradients of the
+ * combine, and the norms around a block with theirs.  Same conventions:
+ * device pointers, one stream, contiguous arrays, host-side return codes, no
+ * device memory allocated.  Every result is the same from call to call (no
+ * atomics), and no output may overlap an input unless said otherwise.
+ *
+ * One step of a layer, with a layout-only moe_dispatch_direct (tokens NULL) in
+ * front and x, y expert-major bf16 rows:
+ *   forwards   moe_combine_grad (y_em, topk_w NULL: the tokens' rows) ->
+ *              moe_ffn_up -> moe_grouped_gemm_bf16 -> moe_combine_pull ->
+ *              moe_block_norm
+ *   backwards  moe_block_norm_grad -> moe_combine_grad -> moe_ffn_up_grad ->
+ *              moe_grouped_gemm_bf16 (transposed), moe_grouped_wgrad twice ->
+ *              moe_combine_pull with weights of 1 (the tokens' gradients)
+ * x need not be kept between the two: the same moe_combine_grad makes it again.
+ *
+ * Row rules of the products, as for moe_grouped_gemm: exp_off int32
+ * [N][E/N+1] from dispatch; rows that it gives to no expert are neither read
+ * nor written; the shape's H must be valid but changes nothing.  Sums are
+ * float32, products of bf16 exact.
+ */
+
+/*
+ * Gate and up product of every expert-major row with its activation, and an
+ * 8-bit checkpoint of the two for moe_ffn_up_grad: for row i of expert e
+ *   g = w13[e][f] . x[i],  u = w13[e][I + f] . x[i],
+ *   a[i][f] = bf16_rne(g / (1 + exp(-g)) * u),
+ *   h_s[i][b] = amax over block b of 128 of [g u] / 448,  h_q = e4m3fn([g u] / h_s)
+ * (quantised from float32 by dispatch's rule; a itself is not rounded to 8 bits).
+ *   x     bf16 [rows][K], 16-B aligned; rows = moe_recv_rows(shape).
+ *   w13   bf16 [E][2*I][K], 16-B aligned: I gate features, then I up features.
+ *   K, I  multiples of 128, 128..32768, else MOE_EINVAL.
+ *   a     bf16 [rows][I] out, 16-B aligned.
+ *   h_q, h_s  fp8 e4m3fn [rows][2*I] out, 16-B aligned, and fp32
+ *         [rows][2*I/128] out, or both NULL (nothing is kept).
+ */
+int moe_ffn_up(const moe_shape *shape, const uint16_t *x, const uint16_t *w13, const int32_t *exp_off, int32_t K,
+               int32_t I, uint16_t *a, uint8_t *h_q, float *h_s, void *stream);
+
+/*
+ * The experts' product in bfloat16: for row i of expert e
+ *   y[i][f] = bf16_rne(sum_c x[i][c] * w[e][f][c])     w_t 0, w [E][F][K]
+ *   y[i][f] = bf16_rne(sum_c x[i][c] * w[e][c][f])     w_t 1, w [E][K][F]
+ * the down product (w2, w_t 0) and the gradient of a product's rows (the
+ * product's own weights, w_t 1).
+ *   x, w, y  bf16, 16-B aligned; x [rows][K], y [rows][F] out.
+ *   K     a multiple of 128, 128..65536; F a multiple of 16, 16..32768.
+ */
+int moe_grouped_gemm_bf16(const moe_shape *shape, const uint16_t *x, const uint16_t *w, const int32_t *exp_off,
+                          int32_t K, int32_t F, int32_t w_t, uint16_t *y, void *stream);
+
+/*
+ * The gradient of moe_ffn_up's rows through its activation and the down
+ * product behind it, from the 8-bit checkpoint: for row i of expert e, with
+ * g and u the checkpoint's values (byte * scale) and s = 1 / (1 + exp(-g)),
+ *   da = sum_c dy[i][c] * w2[e][c][f],
+ *   dh[i][f] = bf16_rne(da * u * s * (1 + g * (1 - s))),  dh[i][I + f] = bf16_rne(da * g * s),
+ *   a[i][f] = bf16_rne(g * s * u).
+ * dh goes to moe_grouped_gemm_bf16 (with w13, w_t 1: the gradient of x) and to
+ * moe_grouped_wgrad (with x: that of w13); a and dy give that of w2.
+ *   dy    bf16 [rows][K], 16-B aligned.
+ *   w2    bf16 [E][K][I], 16-B aligned.
+ *   h_q, h_s  as moe_ffn_up wrote them.
+ *   K, I  multiples of 128, 128..32768, else MOE_EINVAL.
+ *   dh    bf16 [rows][2*I] out, 16-B aligned.
+ *   a     bf16 [rows][I] out, 16-B aligned, or NULL.
+ */
+int moe_ffn_up_grad(const moe_shape *shape, const uint16_t *dy, const uint16_t *w2, const uint8_t *h_q,
+                    const float *h_s, const int32_t *exp_off, int32_t K, int32_t I, uint16_t *dh, uint16_t *a,
+                    void *stream);
+
+/*
+ * The gradient of the experts' weights: for every expert e, over its rows i,
+ *   dw[e][f][c] = sum_i d[i][f] * x[i][c]
+ * with d the gradient of the product's output and x its input.  An expert
+ * without rows gets zeros.
+ *   d, x  bf16 [rows][F], [rows][K], 16-B aligned.
+ *   F     a multiple of 16, 16..65536; K a multiple of 16, 16..32768.
+ *   dw    [E][F][K] out, 16-B aligned: bf16, or fp32 with MOE_WGRAD_F32;
+ *         with MOE_WGRAD_ADD the sum is added in float32 to what dw holds.
+ *   flags 0 or a combination of the two, else MOE_EINVAL.
+ * With fixed regions, a row that an overflow left without a token counts like
+ * any other of its expert: moe_combine_grad writes zeros there.
+ */
+#define MOE_WGRAD_F32 1
+#define MOE_WGRAD_ADD 2
+int moe_grouped_wgrad(const moe_shape *shape, const uint16_t *d, const uint16_t *x, const int32_t *exp_off, int32_t F,
+                      int32_t K, void *dw, int32_t flags, void *stream);
+
+/*
+ * The gradients of the combine, and without weights the dispatch of bf16 rows:
+ * for slot (s,t,j) with expert-major row p (as moe_combine_pull finds it)
+ *   dy_em[p] = bf16_rne(topk_w[s][t][j] * dout[s][t]),
+ *   dtopk_w[s][t][j] = sum_c dout[s][t][c] * y_em[p][c]  (float32; 0 for a slot without a row).
+ *   dout      bf16 [N][T][H], 16-B aligned.
+ *   y_em      bf16 [rows][H], 16-B aligned, the rows that were combined; NULL
+ *             together with dtopk_w.
+ *   topk_idx, send_pos, ws  as for moe_combine_pull.
+ *   topk_w    fp32 [N][T][k], or NULL for weights of 1: dy_em then holds
+ *             every slot's token.
+ *   row_src   int32 [rows] from the dispatch; may be NULL with packed regions.
+ *             With fixed regions, rows that it marks -1 get zeros.
+ *   dy_em     bf16 [rows][H] out, 16-B aligned, or NULL; may be y_em itself.
+ *   dtopk_w   fp32 [N][T][k] out, or NULL.  At least one of the two.
+ * Other rows of dy_em that no slot has are left untouched.
+ */
+int moe_combine_grad(const moe_shape *shape, const uint16_t *dout, const uint16_t *y_em, const int32_t *topk_idx,
+                     const int32_t *send_pos, const float *topk_w, const int32_t *row_src, const void *ws,
+                     uint16_t *dy_em, float *dtopk_w, void *stream);
+
+/*
+ * The norms after and before a block, with the block's gate and the
+ * residual's scale between them: for every token row, rms(v) =
+ * sqrt(mean(v^2) + eps),
+ *   r = alpha * residual + gate * (x / rms(x) * gamma_post),
+ *   y = r / rms(r) * gamma_next
+ * in float32 (r is not rounded on the way), each output rounded once.
+ *   x           bf16 [N][T][H], 16-B aligned: the block's output.
+ *   residual    bf16 [N][T][H], 16-B aligned.
+ *   gamma_post  bf16 [H], 16-B aligned.
+ *   gate        fp32 [N][T], one number per token, or NULL (1).
+ *   alpha, eps  finite; eps above 0; else MOE_EINVAL.
+ *   gamma_next  bf16 [H], 16-B aligned, or NULL together with y.
+ *   res_out     bf16 [N][T][H] out, 16-B aligned: r.
+ *   y           bf16 [N][T][H] out, 16-B aligned: the next block's input.
+ * res_out and y may be x or residual themselves (same start), never a shifted
+ * overlap.  The shape must be a valid one, but its k, E and region_rows
+ * change nothing here; the same holds for moe_block_norm_grad.
+ */
+int moe_block_norm(const moe_shape *shape, const uint16_t *x, const uint16_t *residual, const uint16_t *gamma_post,
+                   const float *gate, float alpha, const uint16_t *gamma_next, float eps, uint16_t *res_out,
+                   uint16_t *y, void *stream);
+
+/*
+ * The gradients of moe_block_norm, from those of its outputs.  r and the
+ * norms are formed again from x and residual, so neither r nor y is needed.
+ *   dy         bf16 [N][T][H], 16-B aligned, or NULL together with gamma_next
+ *              and dgamma_next.
+ *   dres_out   bf16 [N][T][H], 16-B aligned, or NULL.  At least one of the two.
+ *   x, residual, gamma_post, gate, alpha, gamma_next, eps  as they were given.
+ *   dx, dresidual  bf16 [N][T][H] out, 16-B aligned; they may be dy, dres_out,
+ *              x or residual themselves (same start).
+ *   dgate      fp32 [N][T] out (the derivative at the gate given, 1 with
+ *              NULL), or NULL.
+ *   dgamma_post, dgamma_next  fp32 [H] out, sums over all tokens (zeros for
+ *              none).
+ *   ws         moe_block_norm_grad_workspace_bytes(shape) bytes, device, 256-B
+ *              aligned, no initialisation; holds nothing between calls.  Calls
+ *              that share it must be ordered.
+ */
+int64_t moe_block_norm_grad_workspace_bytes(const moe_shape *shape);
+int moe_block_norm_grad(const moe_shape *shape, const uint16_t *dy, const uint16_t *dres_out, const uint16_t *x,
+                        const uint16_t *residual, const uint16_t *gamma_post, const float *gate, float alpha,
+                        const uint16_t *gamma_next, float eps, uint16_t *dx, uint16_t *dresidual, float *dgate,
+                        float *dgamma_post, float *dgamma_next, void *ws, void *stream);
+
 /*
  * Wait for `stream`, return the sticky error bits accumulated in ws since the
  * last call (MOE_FLAG_*) through *flags, and clear them.  The only call that
