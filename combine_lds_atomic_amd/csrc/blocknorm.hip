@@ -12,6 +12,8 @@
 //   dgamma_next = sum over rows of dy * r * i2,      dgamma_post = sum over rows of gate * d * x * i1
 //
 // in float32, each output rounded once.
+#include <algorithm>
+
 #include "moe_internal.h"
 #include "quant_dev.h"
 
@@ -46,18 +48,29 @@ __device__ __forceinline__ void unpack8(const v4u& a, float* f) {
     f[2 * i + 1] = bf16_hi(a[i]);
   }
 }
+// Elements 4h .. 4h + 3 of a unit.
+__device__ __forceinline__ void unpack4(const v4u& a, int h, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[2 * i] = bf16_lo(a[2 * h + i]);
+    f[2 * i + 1] = bf16_hi(a[2 * h + i]);
+  }
+}
 __device__ __forceinline__ v4u pack8(const float* f) {
   v4u o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) o[i] = cvt_bf16(f[2 * i], f[2 * i + 1]);
   return o;
 }
 __device__ __forceinline__ v4u unit(const uint16_t* p, int64_t at, int c) {
   return ld16(reinterpret_cast<const v4u*>(p + at) + c);
 }
 
-// Sums of V values over the threads of a row, the same in all of them.  `part`
-// is used by one sum of a row only.
+// Keeps the compiler from holding what it unpacked from `v` for the next use.
+__device__ __forceinline__ void forget(v4u& v) { asm volatile("" : "+v"(v)); }
+
+// Sums of V values over the threads of a row, the same in all of them.  A
+// barrier lies between one use of `part` and the next.
 template <int V, bool WAVE>
 __device__ __forceinline__ void row_sum(float (&v)[V], float (*part)[V]) {
 #pragma unroll
@@ -75,6 +88,46 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float (*part)[V]) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] += part[w][i];
   }
+}
+
+// v's value from the lane that DPP control `Ctrl` names, added.
+template <int Ctrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(dpp_mov<Ctrl>(__float_as_uint(v)));
+}
+// Over each aligned group of 8 lanes.
+__device__ __forceinline__ float sum8_lanes(float v) {
+  return dpp_add<kDppHalfMirror>(dpp_add<kDppQuadXor2>(dpp_add<kDppQuadXor1>(v)));
+}
+
+// Sums of eight values over the threads of a workgroup of at most 16 waves,
+// as scalars.  Each of the first three steps adds halves of the wave and halves
+// the values that a lane carries; from then on lane i has value i / 8.  All
+// moves between lanes are register moves: through LDS the same chain took 3%
+// of the gradient's time.
+__device__ __forceinline__ void row_sum8(float (&v)[8], float (*part)[8]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+  constexpr int kRowRor8 = 0x128;   // lane i <-> i ^ 8 inside 16 lanes
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 4]), false, false);
+    a[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(a[i + 2]), false, false);
+    b[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  }
+  const float keep = lane & 8 ? b[1] : b[0], give = lane & 8 ? b[0] : b[1];
+  float s = sum8_lanes(keep + __uint_as_float(dpp_mov<kRowRor8>(__float_as_uint(give))));
+  if ((lane & 7) == 0) part[wave][lane >> 3] = s;
+  __syncthreads();
+  s = (lane & 7) < waves ? part[lane & 7][lane >> 3] : 0.0f;
+  if ((lane & 7) + 8 < waves) s += part[(lane & 7) + 8][lane >> 3];
+  s = sum8_lanes(s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s), i * 8));
 }
 
 // A unit is 8 elements: 16 bytes.  Thread i of a row's threads takes units i,
@@ -136,73 +189,154 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 }
 
 // Backwards: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
-// columns' sums of the two dgammas in registers until the last of them.
-template <int U>
+// columns' sums of the two dgammas in registers until the last of them.  With
+// AHEAD the next row's loads are issued before this one is worked on.
+//
+// r is linear in 1 / rms(x), so one reduction of seven sums gives both roots,
+// the part of t along r and dgate, where a reduction after each of them would
+// be three.  The sum of r^2 comes out of its three parts; where the residual
+// and the block's term cancel to less than an eighth of those, it is formed
+// from r itself in a second reduction.
+template <int U, bool AHEAD>
 __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
-  __shared__ float p1[kMaxWaves][1], p2[kMaxWaves][2], p3[kMaxWaves][1];
+  __shared__ float part[2][kMaxWaves][8], one[kMaxWaves][1];
   const int threads = blockDim.x, units = A.H / 8;
+  const v4u zero = {0, 0, 0, 0};
+  const float h = 1.0f / (float)A.H;
   float dgp[U][8], dgn[U][8];
+  v4u gp[U], gn[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    const int c = threadIdx.x + u * threads;
+    gp[u] = c < units ? *(reinterpret_cast<const v4u*>(A.gamma_post) + c) : zero;
+    gn[u] = c < units && A.gamma_next ? *(reinterpret_cast<const v4u*>(A.gamma_next) + c) : zero;
 #pragma unroll
     for (int i = 0; i < 8; ++i) dgp[u][i] = dgn[u][i] = 0.0f;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+  }
+  struct Row {
+    v4u x[U], r[U], t[U], d[U];
+  };
+  auto read = [&](int64_t row, Row& q) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = threadIdx.x + u * threads;
+      const bool in = c < units;
+      q.x[u] = in ? unit(A.x, row * A.H, c) : zero;
+      q.r[u] = in ? unit(A.residual, row * A.H, c) : zero;
+      q.t[u] = in && A.dy ? unit(A.dy, row * A.H, c) : zero;
+      q.d[u] = in && A.dr ? unit(A.dr, row * A.H, c) : zero;
+    }
+  };
+  Row next;
+  if (AHEAD && blockIdx.x < A.rows) read(blockIdx.x, next);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
     const int64_t at = row * A.H;
     const float gate = A.gate ? A.gate[row] : 1.0f;
-    float x[U][8], r[U][8], t[U][8], d[U][8], s1[1] = {0.0f}, s2[2] = {0.0f, 0.0f}, s3[1] = {0.0f};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = threadIdx.x + u * threads;
-      const v4u zero = {0, 0, 0, 0};
-      unpack8(c < units ? unit(A.x, at, c) : zero, x[u]);
-      unpack8(c < units ? unit(A.residual, at, c) : zero, r[u]);
-      unpack8(c < units && A.dy ? unit(A.dy, at, c) : zero, t[u]);
-      unpack8(c < units && A.dr ? unit(A.dr, at, c) : zero, d[u]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s1[0] = __builtin_fmaf(x[u][i], x[u][i], s1[0]);
+    Row q;
+    if constexpr (AHEAD) {
+      q = next;
+      if (row + gridDim.x < A.rows) read(row + gridDim.x, next);
+    } else {
+      read(row, q);
     }
-    row_sum<1, false>(s1, p1);
-    const float i1 = 1.0f / sqrtf(s1[0] / (float)A.H + A.eps);
-    float gp[U][8], gn[U][8];
+    // sums of: x x, (x gp)^2, res res, res x gp, t res, t x gp, dr x gp
+    float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = threadIdx.x + u * threads;
-      const v4u zero = {0, 0, 0, 0};
-      unpack8(c < units ? *(reinterpret_cast<const v4u*>(A.gamma_post) + c) : zero, gp[u]);
-      unpack8(c < units && A.gamma_next ? *(reinterpret_cast<const v4u*>(A.gamma_next) + c) : zero, gn[u]);
+      forget(gp[u]);
+      forget(gn[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[u][i] *= i1;
-        r[u][i] = A.alpha * r[u][i] + gate * (x[u][i] * gp[u][i]);
-        s2[0] = __builtin_fmaf(r[u][i], r[u][i], s2[0]);
-        s2[1] = __builtin_fmaf(t[u][i] * gn[u][i], r[u][i], s2[1]);
+      for (int half = 0; half < 2; ++half) {
+        float x[4], r[4], g[4], n[4], t[4], d[4];
+        unpack4(q.x[u], half, x);
+        unpack4(q.r[u], half, r);
+        unpack4(gp[u], half, g);
+        unpack4(gn[u], half, n);
+        unpack4(q.t[u], half, t);
+        unpack4(q.d[u], half, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float xg = x[i] * g[i], tn = t[i] * n[i];
+          m[0] = __builtin_fmaf(x[i], x[i], m[0]);
+          m[1] = __builtin_fmaf(xg, xg, m[1]);
+          m[2] = __builtin_fmaf(r[i], r[i], m[2]);
+          m[3] = __builtin_fmaf(r[i], xg, m[3]);
+          m[4] = __builtin_fmaf(tn, r[i], m[4]);
+          m[5] = __builtin_fmaf(tn, xg, m[5]);
+          m[6] = __builtin_fmaf(d[i], xg, m[6]);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // few numbers unpacked at a time
       }
     }
-    row_sum<2, false>(s2, p2);
-    const float i2 = 1.0f / sqrtf(s2[0] / (float)A.H + A.eps), along = s2[1] / (float)A.H * i2 * i2;
+    row_sum8(m, part[turn]);
+    const float i1 = rsqrtf(m[0] * h + A.eps), b = gate * i1;
+    const float apart = A.alpha * A.alpha * m[2] + b * b * m[1];
+    float rr = apart + 2.0f * A.alpha * b * m[3];
+    if (!(rr >= 0.125f * apart)) {   // the residual and the block nearly cancel: the sum of r itself
+      float v[1] = {0.0f};
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        float x[8], r[8], g[8];
+        unpack8(q.x[u], x);
+        unpack8(q.r[u], r);
+        unpack8(gp[u], g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[u][i] += i2 * (t[u][i] * gn[u][i] - r[u][i] * along);
-        s3[0] = __builtin_fmaf(d[u][i] * gp[u][i], x[u][i], s3[0]);
-        dgn[u][i] = __builtin_fmaf(t[u][i], r[u][i] * i2, dgn[u][i]);
-        dgp[u][i] = __builtin_fmaf(gate * d[u][i], x[u][i], dgp[u][i]);
+        for (int i = 0; i < 8; ++i) {
+          const float w = A.alpha * r[i] + b * (x[i] * g[i]);
+          v[0] = __builtin_fmaf(w, w, v[0]);
+        }
       }
-    row_sum<1, false>(s3, p3);
-    if (threadIdx.x == 0 && A.dgate) A.dgate[row] = s3[0];
-    const float part = gate * s3[0] / (float)A.H;
+      row_sum<1, false>(v, one);
+      rr = v[0];
+    }
+    const float i2 = rsqrtf(rr * h + A.eps);
+    const float along = (A.alpha * m[4] + b * m[5]) * h * i2 * i2;
+    const float dg = i1 * (m[6] + i2 * (m[5] - along * (A.alpha * m[3] + b * m[1])));
+    if (threadIdx.x == 0 && A.dgate) A.dgate[row] = dg;
+    const float k0 = i1 * i1 * gate * dg * h, k1 = i2 * along;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = threadIdx.x + u * threads;
-      if (c >= units) continue;
+      forget(q.x[u]);
+      forget(q.r[u]);
+      forget(q.t[u]);
+      forget(q.d[u]);
+      forget(gp[u]);
+      forget(gn[u]);
+      v4u dx, dres;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[u][i] = i1 * (gate * d[u][i] * gp[u][i] - x[u][i] * part);
-        d[u][i] *= A.alpha;
+      for (int half = 0; half < 2; ++half) {
+        float x[4], r[4], g[4], n[4], t[4], d[4];
+        unpack4(q.x[u], half, x);
+        unpack4(q.r[u], half, r);
+        unpack4(gp[u], half, g);
+        unpack4(gn[u], half, n);
+        unpack4(q.t[u], half, t);
+        unpack4(q.d[u], half, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r[i] = A.alpha * r[i] + b * (x[i] * g[i]);
+          d[i] = d[i] + i2 * (t[i] * n[i]) - k1 * r[i];
+          float& gn_sum = dgn[u][half * 4 + i];
+          float& gp_sum = dgp[u][half * 4 + i];
+          gn_sum = __builtin_fmaf(t[i], r[i] * i2, gn_sum);
+          const float e = b * d[i];
+          gp_sum = __builtin_fmaf(e, x[i], gp_sum);
+          x[i] = e * g[i] - x[i] * k0;
+          d[i] *= A.alpha;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          dx[2 * half + i] = cvt_bf16(x[2 * i], x[2 * i + 1]);
+          dres[2 * half + i] = cvt_bf16(d[2 * i], d[2 * i + 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      st16(reinterpret_cast<v4u*>(A.o0 + at) + c, pack8(x[u]));
-      st16(reinterpret_cast<v4u*>(A.o1 + at) + c, pack8(d[u]));
+      if (c < units) {
+        st16(reinterpret_cast<v4u*>(A.o0 + at) + c, dx);
+        st16(reinterpret_cast<v4u*>(A.o1 + at) + c, dres);
+      }
     }
   }
   float* out = A.part + (int64_t)blockIdx.x * 2 * A.H;
@@ -211,39 +345,58 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
     const int c = threadIdx.x + u * threads;
     if (c >= units) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      out[c * 8 + i] = dgp[u][i];
-      out[A.H + c * 8 + i] = dgn[u][i];
+    for (int i = 0; i < 8; i += 4) {
+      *reinterpret_cast<float4*>(out + c * 8 + i) = float4{dgp[u][i], dgp[u][i + 1], dgp[u][i + 2], dgp[u][i + 3]};
+      *reinterpret_cast<float4*>(out + A.H + c * 8 + i) = float4{dgn[u][i], dgn[u][i + 1], dgn[u][i + 2], dgn[u][i + 3]};
     }
   }
 }
 
 // The workgroups' sums added up, in their order: 64 columns a workgroup, its
-// four waves taking a quarter of the parts each.
-__global__ __launch_bounds__(256) void k_block_norm_join(const float* __restrict__ part, int parts, int H,
-                                                        float* __restrict__ dgamma_post,
-                                                        float* __restrict__ dgamma_next) {
-  __shared__ float sum[4][kWave];
+// waves taking an equal share of the parts each, eight loads on their way.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(kJoinWaves* kWave) void k_block_norm_join(const float* __restrict__ part, int parts,
+                                                                      int H, float* __restrict__ dgamma_post,
+                                                                      float* __restrict__ dgamma_next) {
+  __shared__ float sum[kJoinWaves][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = blockIdx.x * kWave + lane;   // c < 2H
+  const int end = (int)((int64_t)parts * (wave + 1) / kJoinWaves);
+  const float* at = part + c;
   float s = 0.0f;
-  for (int p = parts * wave / 4; p < parts * (wave + 1) / 4; ++p) s += part[(int64_t)p * 2 * H + c];
+  int p = (int)((int64_t)parts * wave / kJoinWaves);
+  for (; p + 8 <= end; p += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = at[(int64_t)(p + i) * 2 * H];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
+  for (; p < end; ++p) s += at[(int64_t)p * 2 * H];
   sum[wave][lane] = s;
   __syncthreads();
   if (wave) return;
-  s = sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane];
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) s += sum[w][lane];
   float* out = c < H ? dgamma_post : dgamma_next;
   if (out) out[c < H ? c : c - H] = s;
 }
 
+// Units of a thread backwards: the fewest that leave a workgroup of at most
+// 1024 threads.  With two or four, registers are short and some go to scratch.
+inline int grad_units(int H) { return H <= 8 * kMaxThreads ? 1 : H <= 16 * kMaxThreads ? 2 : 4; }
 inline int grad_threads(int H) {
-  const int units = H / 8, u = units <= 2 * kMaxThreads ? 2 : 4;
-  return (units + u * kWave - 1) / (u * kWave) * kWave;
+  const int u = grad_units(H);
+  return (H / 8 + u * kWave - 1) / (u * kWave) * kWave;
 }
 
-// Workgroups of the gradient's first kernel: what 256 compute units hold at once.
+// Workgroups of the gradient's first kernel: what 256 compute units hold at
+// once, but at least four rows each beyond 256 rows, since the sums that a
+// workgroup leaves are as many bytes as one row and a third.
 inline int64_t grad_groups(const Dims& D) {
-  const int64_t rows = (int64_t)D.N * D.T, most = 256 * (2048 / grad_threads(D.H));
-  return rows < most ? rows : most;
+  const int64_t rows = (int64_t)D.N * D.T, most = 256 * (1024 / grad_threads(D.H));
+  if (rows <= 256) return rows;
+  return std::min(std::max<int64_t>(rows / 4, 256), most);
 }
 
 }  // namespace
@@ -308,12 +461,12 @@ int launch_block_norm_grad(const Dims& D, const uint16_t* dy, const uint16_t* dr
   const int64_t groups = grad_groups(D);
   const dim3 threads(grad_threads(D.H));
   if (groups) {
-    const int rc = D.H / 8 <= 2 * kMaxThreads
-                       ? launch("k_block_norm_grad", k_block_norm_grad<2>, dim3((uint32_t)groups), threads, 0, st, A)
-                       : launch("k_block_norm_grad", k_block_norm_grad<4>, dim3((uint32_t)groups), threads, 0, st, A);
+    const int u = grad_units(D.H);
+    const auto k = u == 1 ? k_block_norm_grad<1, true> : u == 2 ? k_block_norm_grad<2, false> : k_block_norm_grad<4, false>;
+    const int rc = launch("k_block_norm_grad", k, dim3((uint32_t)groups), threads, 0, st, A);
     if (rc != MOE_OK) return rc;
   }
-  return launch("k_block_norm_join", k_block_norm_join, dim3(2 * D.H / kWave), dim3(256), 0, st, A.part, (int)groups,
+  return launch("k_block_norm_join", k_block_norm_join, dim3(2 * D.H / kWave), dim3(kJoinWaves * kWave), 0, st, A.part, (int)groups,
                 D.H, dgamma_post, dgamma_next);
 }
 

@@ -30,6 +30,7 @@
 #include <algorithm>
 
 #include "moe_internal.h"
+#include "quant_dev.h"
 
 namespace moe {
 
@@ -546,68 +547,110 @@ __global__ __launch_bounds__(kPsThreads) void k_comb_send_partial(Dims D, Ws W, 
 
 // Gradients of the weighted average: for slot (s,t,j) with expert-major row p,
 //   dy[p] = bf16(w[s][t][j] * dout[s][t]),  dw[s][t][j] = <dout[s][t], y[p]>  (0 without a row).
-// One workgroup per token, wave w taking slots w, w + 4, ...; a lane takes the
-// 16-byte units lane, lane + 64, ... of a row, U of them at a time.  ONE: U
-// covers the row, so the wave reads dout once and keeps it.  y (and dw) or dy
-// may be null, or the same memory; without weights (w null) every weight is 1.
-template <int U, bool ONE>
-__global__ __launch_bounds__(kThreads) void k_comb_grad(Dims D, Ws W, const uint16_t* __restrict__ dout,
-                                                       const uint16_t* y, const int* __restrict__ idx,
-                                                       const int* __restrict__ send_pos,
-                                                       const float* __restrict__ topk_w, uint16_t* dy,
-                                                       float* __restrict__ dw) {
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+// One workgroup of WAVES waves per token.  A thread takes the 16-byte units
+// threadIdx, + 64 WAVES, ... of a row, U of them at a time (all of them if ONE:
+// dout is then read once), and G slots' units are on their way together.  Lane j of every wave looks slot j's row up (k is at most 64), so
+// the routing tables are read once for all slots.  y (and dw) or dy may be null, or
+// the same memory; without weights (w null) every weight is 1.
+//
+// Bound by HBM: rows of two arrays read and written in the order of the
+// routing, 3.11 ms for 65536 tokens, 524288 rows of 7168 (16.0 GB: 5.1 TB/s,
+// where a plain copy reaches 6.7).  Its shape does not matter: 2, 4 and 8
+// slots at a time, workgroups of 2, 4, 7 and 14 waves took 3.11 to 3.24 ms; one
+// wave per slot with all of a row's units on their way 4.0.
+template <int WAVES, int U, int G, bool ONE>
+__global__ __launch_bounds__(WAVES* kWave) void k_comb_grad(Dims D, Ws W, const uint16_t* __restrict__ dout,
+                                                           const uint16_t* y, const int* __restrict__ idx,
+                                                           const int* __restrict__ send_pos,
+                                                           const float* __restrict__ topk_w, uint16_t* dy,
+                                                           float* __restrict__ dw) {
+  constexpr int THREADS = WAVES * kWave;
+  __shared__ float part[WAVES][kMaxK];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int n16 = D.H / 8;
   for (int64_t tok = blockIdx.x; tok < (int64_t)D.N * D.T; tok += gridDim.x) {
     const v4u* __restrict__ ds = reinterpret_cast<const v4u*>(dout) + tok * n16;
-    const int s = (int)(tok / D.T);
+    const int64_t mine = tok * D.k + min(lane, D.k - 1);
     v4u d[U];
     auto read = [&](const v4u* p, int c0, v4u(&v)[U]) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * kWave + lane;
+        const int c = c0 + u * THREADS + (int)threadIdx.x;
         v[u] = c < n16 ? ld16(p + c) : v4u{0, 0, 0, 0};
       }
     };
     if constexpr (ONE) read(ds, 0, d);
-    for (int j = wave; j < D.k; j += kWavesPerBlock) {
-      const int64_t slot = tok * D.k + j;
-      const int row = em_row_of(D, W, s, idx[slot], send_pos[slot]);
-      float dot = 0.0f;
-      if (row >= 0) {
-        const float w = topk_w ? topk_w[slot] : 1.0f;
-        for (int c0 = 0; c0 < n16; c0 += U * kWave) {
-          if constexpr (!ONE) read(ds, c0, d);
-          if (y) {
-            v4u v[U];
-            read(reinterpret_cast<const v4u*>(y) + (int64_t)row * n16, c0, v);
+    const int my_row = em_row_of(D, W, (int)(tok / D.T), idx[mine], send_pos[mine]);
+    const float my_w = topk_w ? topk_w[mine] : 1.0f;
+    for (int j0 = 0; j0 < D.k; j0 += G) {
+      int row[G];
+      float w[G], dot[G];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+      for (int g = 0; g < G; ++g) {
+        const int j = min(j0 + g, D.k - 1);
+        row[g] = j0 + g < D.k ? __builtin_amdgcn_readlane(my_row, j) : -1;
+        w[g] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), j));
+        dot[g] = 0.0f;
+      }
+      for (int c0 = 0; c0 < (ONE ? 1 : n16); c0 += U * THREADS) {
+        if constexpr (!ONE) read(ds, c0, d);
+        if (y) {
+          v4u v[G][U];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                dot = __builtin_fmaf(bf16_lo(d[u][i]), bf16_lo(v[u][i]), dot);
-                dot = __builtin_fmaf(bf16_hi(d[u][i]), bf16_hi(v[u][i]), dot);
-              }
-          }
-          if (dy) {
-            v4u* o = reinterpret_cast<v4u*>(dy) + (int64_t)row * n16;
+          for (int g = 0; g < G; ++g)
+            if (row[g] >= 0) read(reinterpret_cast<const v4u*>(y) + (int64_t)row[g] * n16, c0, v[g]);
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            if (row[g] >= 0) {
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  dot[g] = __builtin_fmaf(bf16_lo(d[u][i]), bf16_lo(v[g][u][i]), dot[g]);
+                  dot[g] = __builtin_fmaf(bf16_hi(d[u][i]), bf16_hi(v[g][u][i]), dot[g]);
+                }
+            }
+        }
+        if (dy) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            if (row[g] < 0) continue;
+            v4u* o = reinterpret_cast<v4u*>(dy) + (int64_t)row[g] * n16;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-              const int c = c0 + u * kWave + lane;
+              const int c = c0 + u * THREADS + (int)threadIdx.x;
               v4u r;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                r[i] = f32_to_bf16_rne(w * bf16_lo(d[u][i])) | (f32_to_bf16_rne(w * bf16_hi(d[u][i])) << 16);
+              for (int i = 0; i < 4; ++i) r[i] = cvt_bf16(w[g] * bf16_lo(d[u][i]), w[g] * bf16_hi(d[u][i]));
               if (c < n16) st16(o + c, r);
             }
           }
         }
       }
       if (dw) {
+        // G sums over the wave: each halving step leaves a lane half of the sums it had
+        float a[G];
 #pragma unroll
-        for (int m = 1; m < kWave; m <<= 1) dot += __shfl_xor(dot, m);
-        if (lane == 0) dw[slot] = dot;
+        for (int g = 0; g < G; ++g) a[g] = dot[g];
+        int m = kWave / 2;
+#pragma unroll
+        for (int n = G / 2; n; n /= 2, m /= 2)
+#pragma unroll
+          for (int g = 0; g < n; ++g) a[g] = (lane & m ? a[g + n] : a[g]) + __shfl_xor(lane & m ? a[g] : a[g + n], m);
+        for (; m; m /= 2) a[0] += __shfl_xor(a[0], m);
+        const int j = j0 + lane / (kWave / G);
+        if (lane % (kWave / G) == 0 && j < D.k) part[wave][j] = a[0];
       }
+    }
+    if (dw) {
+      if (WAVES > 1) __syncthreads();
+      if ((int)threadIdx.x < D.k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) s += part[i][threadIdx.x];
+        dw[tok * D.k + threadIdx.x] = s;
+      }
+      __syncthreads();
     }
   }
 }
@@ -660,10 +703,16 @@ int launch_comb_grad(const Dims& D, const Ws& W, const uint16_t* dout, const uin
                      hipStream_t st) {
   const int64_t tokens = (int64_t)D.N * D.T;
   if (tokens == 0) return MOE_OK;
-  const int per = (D.H / 8 + kWave - 1) / kWave;   // units of a lane
-  const auto k = per <= 2 ? k_comb_grad<2, true> : per <= 4 ? k_comb_grad<4, true> : per <= 8 ? k_comb_grad<8, true>
-                 : per <= 16 ? k_comb_grad<16, true> : k_comb_grad<16, false>;
-  const int rc = launch("k_comb_grad", k, dim3(os_grid(tokens, 1)), dim3(kThreads), 0, st, D, W, dout, y, idx,
+  // Threads for four units of a row each, up to four waves.
+  const int units = D.H / 8;
+  const int waves = units <= 4 * kWave ? 1 : units <= 8 * kWave ? 2 : 4;
+  const auto k = units <= kWave        ? k_comb_grad<1, 1, 4, true>
+                 : units <= 2 * kWave  ? k_comb_grad<1, 2, 4, true>
+                 : units <= 4 * kWave  ? k_comb_grad<1, 4, 4, true>
+                 : units <= 8 * kWave  ? k_comb_grad<2, 4, 4, true>
+                 : units <= 16 * kWave ? k_comb_grad<4, 4, 4, true>
+                                       : k_comb_grad<4, 4, 4, false>;
+  const int rc = launch("k_comb_grad", k, dim3(os_grid(tokens, 1)), dim3(waves * kWave), 0, st, D, W, dout, y, idx,
                         send_pos, w, dy, dw);
   if (rc || !D.R || !dy) return rc;
   return launch("k_comb_zero_holes", k_comb_zero_holes, dim3((uint32_t)std::min<int64_t>((D.rows + kThreads - 1) / kThreads, 4096)),
