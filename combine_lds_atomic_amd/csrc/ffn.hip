@@ -108,17 +108,21 @@ struct Reader {
 };
 
 // One workgroup: BM left features x up to BN right rows, WM x WN waves of
-// MT x NT matrix tiles; S stages of both operands in LDS.
-template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int S, int EPL>
+// MT x NT matrix tiles; SL and SR stages of the operands in LDS.
+template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int SL, int SR, int EPL>
 __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   constexpr bool RC = EPI == Epi::kWgrad;
   constexpr int NW = WM * WN, THREADS = NW * kWave;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LL = BM * kStepBytes / 1024 / NW, LR = BN * kStepBytes / 1024 / NW;   // loads of a wave and stage
+  constexpr int LPS = LL + LR;
   static_assert(LL * NW * 1024 == BM * kStepBytes && LR * NW * 1024 == BN * kStepBytes, "loads split evenly");
+  static_assert(MT % (EPI == Epi::kUp ? 4 : 2) == 0, "the epilogue takes tiles in pairs");
   static_assert(EPI != Epi::kUp || BM == 2 * kScaleBlock, "a gate and an up half of one scale block");
-  constexpr int kLeft = BM * kStepBytes, kStage = (BM + BN) * kStepBytes;
-  __shared__ __align__(1024) unsigned char lds[S * kStage];
+  static_assert(SR == SL || SR == SL + 1, "the right operand's loads are a step's last");
+  constexpr int kLeft = BM * kStepBytes, kRight = BN * kStepBytes;   // bytes of a stage
+  __shared__ __align__(1024) unsigned char lds[SL * kLeft + SR * kRight];
+  unsigned char* const lds_r = lds + SL * kLeft;
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -129,13 +133,13 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   int e, row, n, ft, gt = 0, KB;     // expert, first right row, right rows, left tile, right tile, K steps
   int rem = kBK;                     // wgrad: rows of the last step
   if constexpr (RC) {
-    // Tiles expert after expert; within one, groups of 4 right tiles, those fastest.
-    const int ng = (A.G + BN - 1) / BN, per = nf * ng;
-    const int64_t total = (int64_t)A.E * per, share = (total + 7) / 8;
-    const int64_t t = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
-    if ((int64_t)(blockIdx.x >> 3) >= share || t >= total) return;
-    e = (int)(t / per);
-    int x = (int)(t - (int64_t)e * per);
+    // Expert after expert; each XCD (workgroup b runs on XCD b % 8) takes an
+    // eighth of every expert's tiles, so that an expert with many rows keeps all of
+    // them busy.  Within an expert groups of 4 right tiles, those fastest.
+    const int ng = (A.G + BN - 1) / BN, per = nf * ng, share = (per + 7) / 8;
+    e = (int)((blockIdx.x >> 3) / (uint32_t)share);
+    int x = (int)(blockIdx.x & 7) * share + (int)((blockIdx.x >> 3) - (uint32_t)e * (uint32_t)share);
+    if (x >= per) return;
     const int g0 = x / (4 * nf) * 4, gs = min(4, ng - g0);
     x -= g0 * nf;
     gt = g0 + x % gs;
@@ -184,29 +188,26 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
 #pragma unroll
     for (int i = 0; i < LR; ++i) roff[i] = col_off(BN, i, gt * BN, A.G);
   }
-  auto issue = [&](int kb) {
-    unsigned char* dst = lds + (kb % S) * kStage + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < LL; ++i) {
-      if constexpr (RC) {
-        const int r = min(col_row(BM, i), n - 1 - kb * kBK);
-        load_lds16(lbase + (int64_t)kb * kBK * A.F, loff[i] + (uint32_t)r * (uint32_t)A.F * 2u, dst + i * NW * 1024);
-      } else if constexpr (LC) {
-        load_lds16(lbase + (int64_t)kb * kBK * A.F, loff[i], dst + i * NW * 1024);
-      } else {
-        load_lds16(lbase + kb * kBK, loff[i], dst + i * NW * 1024);
-      }
+  // The i-th of the wave's loads of the left operand's stage kb, and of the right one's.
+  auto issue_left = [&](int kb, int i) {
+    unsigned char* dst = lds + (kb % SL) * kLeft + (i * NW + wave) * 1024;
+    if constexpr (RC) {
+      const int r = min(col_row(BM, i), n - 1 - kb * kBK);
+      load_lds16(lbase + (int64_t)kb * kBK * A.F, loff[i] + (uint32_t)r * (uint32_t)A.F * 2u, dst);
+    } else if constexpr (LC) {
+      load_lds16(lbase + (int64_t)kb * kBK * A.F, loff[i], dst);
+    } else {
+      load_lds16(lbase + kb * kBK, loff[i], dst);
     }
-#pragma unroll
-    for (int i = 0; i < LR; ++i) {
-      if constexpr (RC) {
-        const int r = min(col_row(BN, i), n - 1 - kb * kBK);
-        load_lds16(rbase + (int64_t)kb * kBK * A.G, roff[i] + (uint32_t)r * (uint32_t)A.G * 2u,
-                   dst + kLeft + i * NW * 1024);
-      } else {
-        const uint32_t r = min(i * NW * 8 + r0, (uint32_t)n - 1u);
-        load_lds16(rbase + kb * kBK, r * (uint32_t)A.K * 2u + c0, dst + kLeft + i * NW * 1024);
-      }
+  };
+  auto issue_right = [&](int kb, int i) {
+    unsigned char* dst = lds_r + (kb % SR) * kRight + (i * NW + wave) * 1024;
+    if constexpr (RC) {
+      const int r = min(col_row(BN, i), n - 1 - kb * kBK);
+      load_lds16(rbase + (int64_t)kb * kBK * A.G, roff[i] + (uint32_t)r * (uint32_t)A.G * 2u, dst);
+    } else {
+      const uint32_t r = min(i * NW * 8 + r0, (uint32_t)n - 1u);
+      load_lds16(rbase + kb * kBK, r * (uint32_t)A.K * 2u + c0, dst);
     }
   };
 
@@ -217,8 +218,14 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
     for (int j = 0; j < NT; ++j) acc[m][j] = v4f{0, 0, 0, 0};
 
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-    if (s < KB) issue(s);
+  for (int s = 0; s < SR; ++s) {
+    if (s >= KB) break;
+    if (s < SL)
+#pragma unroll
+      for (int i = 0; i < LL; ++i) issue_left(s, i);
+#pragma unroll
+    for (int i = 0; i < LR; ++i) issue_right(s, i);
+  }
 
   Reader<LC, BM> rl;
   Reader<RC, BN> rr;
@@ -233,133 +240,200 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
     return EPI == Epi::kUp ? (m < MT / 2 ? wm * (MT / 2) + m : BF / 16 + wm * (MT / 2) + m - MT / 2) : wm * MT + m;
   };
 
-  auto steps = [&](auto nl) {
-    constexpr int NL = decltype(nl)::value;
-    for (int kb = 0; kb < KB; ++kb) {
-      if (S > 2 && kb + S - 1 <= KB) wait_and_barrier<(S - 2) * (LL + LR)>();
-      else wait_and_barrier<0>();
-      unsigned char* st = lds + (kb % S) * kStage;
-      if constexpr (RC) {
-        if (kb == KB - 1 && rem < kBK) {   // rows behind the expert's last count as zeros
-          for (int u = rem * (BM / 8) + threadIdx.x; u < kBK * (BM / 8); u += THREADS)
-            reinterpret_cast<v4u*>(st)[u] = v4u{0, 0, 0, 0};
-          for (int u = rem * (BN / 8) + threadIdx.x; u < kBK * (BN / 8); u += THREADS)
-            reinterpret_cast<v4u*>(st + kLeft)[u] = v4u{0, 0, 0, 0};
-          wait_and_barrier<0>();
-        }
-      }
-      const bool more = kb + S - 1 < KB;
-      if constexpr (NL == 0) {
-        if (more) issue(kb + S - 1);
-      } else {
-        // The next stage is asked for behind this step's first LDS reads.
-        v8bf b[2][NL], a[2];
-#pragma unroll
-        for (int j = 0; j < NL; ++j) b[0][j] = rr.load(st + kLeft, j * WN + wn, 0);
-        a[0] = rl.load(st, ltile(0), 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) issue(kb + S - 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int i = kh * MT + m;
-            if (i + 1 < 2 * MT) a[(i + 1) & 1] = rl.load(st, ltile((i + 1) % MT), (i + 1) / MT);
-            if (kh == 0 && m == MT / 2) {
-#pragma unroll
-              for (int j = 0; j < NL; ++j) b[1][j] = rr.load(st + kLeft, j * WN + wn, 1);
-            }
-#pragma unroll
-            for (int j = 0; j < NL; ++j)
-              acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i & 1], b[kh][j], acc[m][j], 0, 0, 0);
-          }
-        }
+  // Stage kb is in LDS for all waves, with zeros behind the expert's last row;
+  // what was asked for after it may be on its way: SL - 2 stages of the left
+  // operand and SR - 2 of the right one.
+  auto arrived = [&](int kb) {
+    constexpr int kLater = (SL - 2) * LL + (SR - 2) * LR;
+    if (kLater > 0 && kb + SR - 2 < KB) wait_and_barrier<kLater>();
+    else wait_and_barrier<0>();
+    if constexpr (RC) {
+      if (kb == KB - 1 && rem < kBK) {
+        unsigned char *l = lds + (kb % SL) * kLeft, *r = lds_r + (kb % SR) * kRight;
+        for (int u = rem * (BM / 8) + threadIdx.x; u < kBK * (BM / 8); u += THREADS)
+          reinterpret_cast<v4u*>(l)[u] = v4u{0, 0, 0, 0};
+        for (int u = rem * (BN / 8) + threadIdx.x; u < kBK * (BN / 8); u += THREADS)
+          reinterpret_cast<v4u*>(r)[u] = v4u{0, 0, 0, 0};
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
     }
   };
-  static_assert(NT <= 4, "a loop for each number of live tiles");
-  if (live == NT) steps(std::integral_constant<int, NT>());
-  else if (NT > 3 && live == 3) steps(std::integral_constant<int, NT < 3 ? NT : 3>());
-  else if (NT > 2 && live == 2) steps(std::integral_constant<int, NT < 2 ? NT : 2>());
-  else if (NT > 1 && live == 1) steps(std::integral_constant<int, 1>());
-  else steps(std::integral_constant<int, 0>());
+
+  // Two halves of 32 columns a step.  While one half's products run, the
+  // operands of the next are read: those of the step's second half during the
+  // first, those of the next step's first half during the second.  So the one
+  // barrier of a step stands in its middle, where every wave has read all of the
+  // stage, and the loads of step kb + SL (SR) go into it from there on.
+  auto steps = [&](auto nl) {
+    constexpr int NL = decltype(nl)::value;
+    constexpr int kReads = NL + MT, kProducts = MT * NL;
+    v8bf a[2][MT], b[2][NL > 0 ? NL : 1];
+    auto read = [&](int kb, int kh, int i) {   // the i-th operand of a half
+      if (i < NL) b[kh][i] = rr.load(lds_r + (kb % SR) * kRight, i * WN + wn, kh);
+      else a[kh][i - NL] = rl.load(lds + (kb % SL) * kLeft, ltile(i - NL), kh);
+    };
+    // A half's products with `ops` reads and loads spread evenly between them, in
+    // this order: a wave issues in order, and a row of reads would leave its
+    // matrix pipe without work.
+    auto half = [&](auto kh, auto ops, auto op) {
+      constexpr int H = decltype(kh)::value, N = decltype(ops)::value;
+      if constexpr (NL == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) op(i);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kProducts; ++q) {
+#pragma unroll
+          for (int i = q * N / kProducts; i < (q + 1) * N / kProducts; ++i) op(i);
+          const int m = q / NL, j = q % NL;
+          acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[H][m], b[H][j], acc[m][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    constexpr std::integral_constant<int, 0> first{};
+    constexpr std::integral_constant<int, 1> second{};
+    auto step = [&](int kb, auto next, auto left, auto right) {   // which of the later stages there are
+      constexpr int R = NL > 0 ? kReads : 0, LD = (left ? LL : 0) + (right ? LR : 0);
+      half(first, std::integral_constant<int, R>(), [&](int i) { read(kb, 1, i); });
+      if constexpr (next) arrived(kb + 1);
+      // reads and loads in turn, the loads of the left operand first
+      half(second, std::integral_constant<int, (next ? R : 0) + LD>(), [&](int i) {
+        constexpr int Rn = next ? R : 0, N = Rn + LD;
+        const int r0 = i * Rn / N, r1 = (i + 1) * Rn / N;
+        if (r1 > r0) read(kb + 1, 0, r0);
+        else if (i - r0 < LL && left) issue_left(kb + SL, i - r0);
+        else issue_right(kb + SR, i - r0 - (left ? LL : 0));
+      });
+    };
+    if (KB == 0) return;
+    arrived(0);
+    if constexpr (NL > 0) {
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) read(0, 0, i);
+    }
+    int kb = 0;
+    for (; kb + SR < KB; ++kb) step(kb, std::true_type(), std::true_type(), std::true_type());
+    for (; kb + SL < KB; ++kb) step(kb, std::true_type(), std::true_type(), std::false_type());
+    for (; kb + 1 < KB; ++kb) step(kb, std::true_type(), std::false_type(), std::false_type());
+    step(kb, std::false_type(), std::false_type(), std::false_type());
+  };
+  // A loop for each number of live tiles.
+  auto pick = [&](auto self, auto nl) -> void {
+    constexpr int NL = decltype(nl)::value;
+    if (live >= NL) steps(nl);
+    else if constexpr (NL > 0) self(self, std::integral_constant<int, NL - 1>());
+  };
+  pick(pick, std::integral_constant<int, NT>());
 
   // No load may be on its way to LDS that the epilogue, or another workgroup, uses.
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-  // ---- epilogue: lane holds features 16 ltile(m) + 4 (lane/16) + i of right row tok
-  const int tok0 = wn * 16 + (lane & 15), f4 = (lane >> 4) * 4;
+  // ---- epilogue: acc[m][j] holds features 16 ltile(m) + 4 (lane / 16) + i of
+  // right row tok0 + 16 WN j.  Lanes 16 apart trade halves of two neighbouring
+  // tiles, so that a lane has eight consecutive features (f8 on from the first
+  // tile's) and four lanes 64 consecutive bytes of a bf16 row: eight[0..7] of
+  // the pair m, m + 1.
+  const int tok0 = wn * 16 + (lane & 15), f8 = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  auto pair = [&](int m, int j, float (&eight)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[m][j][i]), __float_as_uint(acc[m + 1][j][i]),
+                                                      false, false);
+      eight[i] = __uint_as_float(w[0]);
+      eight[4 + i] = __uint_as_float(w[1]);
+    }
+  };
+  auto rounded = [](const float (&v)[8]) {
+    return v4u{cvt_bf16(v[0], v[1]), cvt_bf16(v[2], v[3]), cvt_bf16(v[4], v[5]), cvt_bf16(v[6], v[7])};
+  };
   if constexpr (EPI == Epi::kPlain) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int tok = tok0 + j * WN * 16;
-      if (tok >= n) continue;
       uint16_t* yr = static_cast<uint16_t*>(A.y) + (int64_t)(row + tok) * A.F;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int f = ft * BM + ltile(m) * 16 + f4;
-        if (f < A.F)
-          *reinterpret_cast<uint2*>(yr + f) =
-              uint2{pack_bf16(acc[m][j][0], acc[m][j][1]), pack_bf16(acc[m][j][2], acc[m][j][3])};
+      for (int m = 0; m < MT; m += 2) {
+        const int f = ft * BM + ltile(m) * 16 + f8;
+        float v[8];
+        pair(m, j, v);
+        if (tok < n && f < A.F) *reinterpret_cast<v4u*>(yr + f) = rounded(v);
       }
     }
   } else if constexpr (EPI == Epi::kWgrad) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int g = gt * BN + tok0 + j * WN * 16;
-      if (g >= A.G) continue;
       const int64_t at = ((int64_t)e * A.G + g) * A.F;
+      if (A.f32) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int f = ft * BM + ltile(m) * 16 + f4;
-        if (f >= A.F) continue;
-        if (A.f32) {
+        for (int m = 0; m < MT; ++m) {
+          const int f = ft * BM + ltile(m) * 16 + (lane >> 4) * 4;
+          if (g >= A.G || f >= A.F) continue;
           v4f* p = reinterpret_cast<v4f*>(static_cast<float*>(A.y) + at + f);
           v4f v = acc[m][j];
           if (A.add) v += *p;
           *p = v;
-        } else {
-          uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + at + f);
-          v4f v = acc[m][j];
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; m += 2) {
+          const int f = ft * BM + ltile(m) * 16 + f8;
+          float v[8];
+          pair(m, j, v);
+          if (g >= A.G || f >= A.F) continue;
+          v4u* p = reinterpret_cast<v4u*>(static_cast<uint16_t*>(A.y) + at + f);
           if (A.add) {
-            const uint2 o = *p;
-            v += v4f{bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y)};
+            const v4u o = *p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] += bf16_lo(o[i]);
+              v[2 * i + 1] += bf16_hi(o[i]);
+            }
           }
-          *p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+          *p = rounded(v);
         }
       }
     }
   } else if constexpr (EPI == Epi::kUpGrad) {
+    // All of a column's checkpoint is asked for before the first of it is used.
+    typedef unsigned int v2u __attribute__((ext_vector_type(2)));
     const int nfb = A.F / kScaleBlock;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int tok = tok0 + j * WN * 16;
-      if (tok >= n) continue;
-      const int64_t r = row + tok;
+      const int64_t r = row + min(tok, n - 1);
       const uint8_t* hq = A.h_q + r * 2 * A.F;
       const float* hs = A.h_s + r * 2 * nfb;
       uint16_t* dh = static_cast<uint16_t*>(A.y) + r * 2 * A.F;
+      v2u gq[MT / 2], uq[MT / 2];
+      float gs[MT / 2], us[MT / 2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int f = ft * BM + ltile(m) * 16 + f4;
-        if (f >= A.F) continue;
-        const uint32_t gq = *reinterpret_cast<const uint32_t*>(hq + f);
-        const uint32_t uq = *reinterpret_cast<const uint32_t*>(hq + A.F + f);
-        const float gs = hs[f / kScaleBlock], us = hs[nfb + f / kScaleBlock];
-        float dg[4], du[4], av[4];
+      for (int p = 0; p < MT / 2; ++p) {
+        const int f = min(ft * BM + ltile(2 * p) * 16 + f8, A.F - 8);
+        gq[p] = *reinterpret_cast<const v2u*>(hq + f);
+        uq[p] = *reinterpret_cast<const v2u*>(hq + A.F + f);
+        gs[p] = hs[f / kScaleBlock];
+        us[p] = hs[nfb + f / kScaleBlock];
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float g = fp8_value(gq, i) * gs, u = fp8_value(uq, i) * us, da = acc[m][j][i];
-          const float s = 1.0f / (1.0f + __expf(-g)), gs1 = g * s;
-          du[i] = da * gs1;
-          dg[i] = da * u * (s * (1.0f + g * (1.0f - s)));
-          av[i] = gs1 * u;
+      for (int p = 0; p < MT / 2; ++p) {
+        const int f = ft * BM + ltile(2 * p) * 16 + f8;
+        float da[8], dg[8], du[8], av[8];
+        pair(2 * p, j, da);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = fp8_value(gq[p][i / 4], i & 3) * gs[p], u = fp8_value(uq[p][i / 4], i & 3) * us[p];
+          const float s = 1.0f / (1.0f + __expf(-g)), y = g * s;
+          du[i] = da[i] * y;
+          dg[i] = da[i] * u * (s * (1.0f + g * (1.0f - s)));
+          av[i] = y * u;
         }
-        *reinterpret_cast<uint2*>(dh + f) = uint2{pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3])};
-        *reinterpret_cast<uint2*>(dh + A.F + f) = uint2{pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3])};
-        if (A.a)
-          *reinterpret_cast<uint2*>(A.a + r * A.F + f) = uint2{pack_bf16(av[0], av[1]), pack_bf16(av[2], av[3])};
+        if (tok < n && f < A.F) {
+          *reinterpret_cast<v4u*>(dh + f) = rounded(dg);
+          *reinterpret_cast<v4u*>(dh + A.F + f) = rounded(du);
+          if (A.a) *reinterpret_cast<v4u*>(A.a + r * A.F + f) = rounded(av);
+        }
       }
     }
   } else {
@@ -373,18 +447,22 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
       const int tok = tok0 + j * WN * 16;
       int mg = 0, mu = 0;
 #pragma unroll
-      for (int m = 0; m < MT / 2; ++m) {
-        float v[4];
+      for (int m = 0; m < MT / 2; m += 2) {
+        float g[8], u[8], v[8];
+        pair(m, j, g);
+        pair(m + MT / 2, j, u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float g = acc[m][j][i], u = acc[m + MT / 2][j][i];
-          v[i] = g / (1.0f + __expf(-g)) * u;
-          mg = max(mg, abs_bits(g));
-          mu = max(mu, abs_bits(u));
+        for (int i = 0; i < 8; ++i) {
+          v[i] = g[i] / (1.0f + __expf(-g[i])) * u[i];
+          mg = max(mg, abs_bits(g[i]));
+          mu = max(mu, abs_bits(u[i]));
+          // kept in the new order
+          acc[m + i / 4][j][i & 3] = g[i];
+          acc[m + MT / 2 + i / 4][j][i & 3] = u[i];
         }
         if (tok < n)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + (int64_t)(row + tok) * A.F + ft * BF +
-                                    ltile(m) * 16 + f4) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+          *reinterpret_cast<v4u*>(static_cast<uint16_t*>(A.y) + (int64_t)(row + tok) * A.F + ft * BF + ltile(m) * 16 +
+                                  f8) = rounded(v);
       }
       mg = max(mg, __shfl_xor(mg, 16));
       mg = max(mg, __shfl_xor(mg, 32));
@@ -408,12 +486,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
         const float scale = block_scale(am);
         if (wm == 0 && lane < 16 && tok < n) A.h_s[((int64_t)(row + tok) * 2 + half) * nfb + ft] = scale;
 #pragma unroll
-        for (int m = 0; m < MT / 2; ++m) {
-          const v4f& c = acc[m + half * (MT / 2)][j];
-          float v[4] = {c[0], c[1], c[2], c[3]};
-          const int col = ltile(m) * 16 + f4;
-          *reinterpret_cast<uint32_t*>(stage + tok * 256 + half * 128 + (((col >> 4) ^ (tok & 7)) << 4) + (col & 15)) =
-              quant4_scaled(v, scale);
+        for (int m = 0; m < MT / 2; m += 2) {
+          const v4f &c = acc[m + half * (MT / 2)][j], &d = acc[m + 1 + half * (MT / 2)][j];
+          const float v[8] = {c[0], c[1], c[2], c[3], d[0], d[1], d[2], d[3]};
+          const int col = ltile(m) * 16 + f8;
+          *reinterpret_cast<uint2*>(stage + tok * 256 + half * 128 + (((col >> 4) ^ (tok & 7)) << 4) + (col & 15)) =
+              uint2{quant4_scaled(v, scale), quant4_scaled(v + 4, scale)};
         }
       }
     }
@@ -427,7 +505,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   }
 }
 
-template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int S>
+template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int SL, int SR>
 int launch_rows(ProductArgs A, int64_t slots, int cus, hipStream_t st) {
   constexpr int BF = EPI == Epi::kUp ? BM / 2 : BM, kThreadsHere = WM * WN * kWave;
   const int64_t active = slots < A.E ? slots : A.E;
@@ -436,8 +514,8 @@ int launch_rows(ProductArgs A, int64_t slots, int cus, hipStream_t st) {
   const int64_t tiles = (slots / A.bn + active) * nf;   // no fewer than the rows can need
   const int64_t grid = (tiles + 7) / 8 * 8;
   if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
-  const auto k = A.E <= 4 * kWave ? k_ffn_product<EPI, LC, BM, BN, WM, WN, S, 4>
-                                  : k_ffn_product<EPI, LC, BM, BN, WM, WN, S, 16>;
+  const auto k = A.E <= 4 * kWave ? k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 4>
+                                  : k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 16>;
   return launch("k_ffn_product", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 
@@ -446,9 +524,18 @@ int launch_any(const ProductArgs& A, int64_t slots, int cus, hipStream_t st) {
   constexpr int BF = EPI == Epi::kUp ? 128 : 256;
   const int64_t active = slots < A.E ? slots : A.E, avg = slots / active;
   const int64_t big = active * ((avg + 255) / 256) * ((A.F + BF - 1) / BF);   // tiles of 256 rows
-  if (avg > 256 && big >= 2 * cus) return launch_rows<EPI, LC, 256, 256, 2, 4, 2>(A, slots, cus, st);
-  if (avg > 48) return launch_rows<EPI, LC, 256, 128, 4, 2, 2>(A, slots, cus, st);
-  return launch_rows<EPI, LC, 256, 32, 4, 1, 2>(A, slots, cus, st);
+  if (avg > 256 && big >= 2 * cus) return launch_rows<EPI, LC, 256, 256, 2, 4, 2, LC ? 2 : 3>(A, slots, cus, st);
+  if (avg > 48) return launch_rows<EPI, LC, 256, 128, 4, 2, 3, 3>(A, slots, cus, st);
+  return launch_rows<EPI, LC, 256, 32, 4, 1, 3, 3>(A, slots, cus, st);
+}
+
+template <int BM, int BN, int WM, int WN>
+int launch_wgrad(const ProductArgs& A, hipStream_t st) {
+  constexpr int kThreadsHere = WM * WN * kWave;
+  const int64_t per = (int64_t)((A.F + BM - 1) / BM) * ((A.G + BN - 1) / BN), grid = (per + 7) / 8 * 8 * A.E;
+  if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
+  return launch("k_ffn_product", k_ffn_product<Epi::kWgrad, true, BM, BN, WM, WN, 2, 2, 1>, dim3((uint32_t)grid),
+                dim3(kThreadsHere), 0, st, A);
 }
 
 ProductArgs base_args(const Dims& D, const uint16_t* left, const uint16_t* right, const int* exp_off, void* y, int K,
@@ -500,11 +587,7 @@ int launch_grouped_wgrad(const Dims& D, const uint16_t* d, const uint16_t* x, co
   A.G = F;
   A.f32 = f32;
   A.add = add;
-  const int64_t tiles = (int64_t)A.E * ((A.F + 255) / 256) * ((A.G + 255) / 256);
-  const int64_t grid = (tiles + 7) / 8 * 8;
-  if (grid * 512 > UINT32_MAX) return MOE_ERANGE;
-  return launch("k_ffn_product", k_ffn_product<Epi::kWgrad, true, 256, 256, 2, 4, 2, 1>, dim3((uint32_t)grid),
-                dim3(512), 0, st, A);
+  return launch_wgrad<256, 256, 2, 4>(A, st);
 }
 
 }  // namespace moe
