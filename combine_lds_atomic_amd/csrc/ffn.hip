@@ -107,6 +107,9 @@ struct Reader {
   }
 };
 
+// 1 / (1 + exp(-g)); the reciprocal instruction is off by one unit in the last place.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
 // One workgroup: BM left features x up to BN right rows, WM x WN waves of
 // MT x NT matrix tiles; SL and SR stages of the operands in LDS.
 template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int SL, int SR, int EPL>
@@ -424,7 +427,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = fp8_value(gq[p][i / 4], i & 3) * gs[p], u = fp8_value(uq[p][i / 4], i & 3) * us[p];
-          const float s = 1.0f / (1.0f + __expf(-g)), y = g * s;
+          const float s = sigmoid(g), y = g * s;
           du[i] = da[i] * y;
           dg[i] = da[i] * u * (s * (1.0f + g * (1.0f - s)));
           av[i] = y * u;
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
         pair(m + MT / 2, j, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = g[i] / (1.0f + __expf(-g[i])) * u[i];
+          v[i] = g[i] * sigmoid(g[i]) * u[i];
           mg = max(mg, abs_bits(g[i]));
           mu = max(mu, abs_bits(u[i]));
           // kept in the new order
