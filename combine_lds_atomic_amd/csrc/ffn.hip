@@ -110,8 +110,26 @@ struct Reader {
 // 1 / (1 + exp(-g)); the reciprocal instruction is off by one unit in the last place.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// One workgroup: BM left features x up to BN right rows, WM x WN waves of
-// MT x NT matrix tiles; SL and SR stages of the operands in LDS.
+// One workgroup forms BM left features x up to BN right rows of one expert:
+// WM x WN waves of MT x NT matrix tiles of 16 x 16, so a lane holds four
+// neighbouring features of one row.  Steps of 64 columns; SL and SR stages of
+// the operands sit in LDS, filled by loads that bypass the registers.
+//
+// What bounds it on MI355X (2048 rows for each of 32 experts, H = 7168, I =
+// 2048, runs on four machines): up 3.30 to 3.39 ms (1.14 to 1.17 PFLOP/s), down 1.65
+// to 1.72, the transposed product 3.12 to 3.32 (1.16 to 1.23), up gradient 1.88
+// to 1.96 (0.98 to 1.02), weight gradients 3.23 and 1.58 (1.19 to 1.22); large
+// library products of the three layouts reach 1.60 (rows x rows), 1.38 and 1.18.
+// The matrix pipes are busy 54% to 61% of the cycles at a clock that falls to
+// 1.9 GHz; LDS reads have no bank conflicts.  A timing copy whose loads stay on
+// two steps (so in L2) took 3.00 ms against 3.57 for up and 3.02 against 3.33
+// transposed, one without the loop's loads 2.68 and 2.66; so a sixth of the time is
+// the way to memory, and deeper stages are what helped (a 256 x 128 tile with three
+// stages against two: 3.99 ms against 4.85).  An epilogue is 128 to 512 KiB a
+// tile that all compute units write at the same time.  Tried and slower: four
+// waves of 128 x 128 (3.9 to 4.4 ms up, whatever the order of its reads), steps of 32
+// columns with four or five stages (3.70), non-temporal stores of y (down
+// 1.72 against 1.65) and of weight gradients (3.46 against 3.32).
 template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int SL, int SR, int EPL>
 __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   constexpr bool RC = EPI == Epi::kWgrad;
@@ -270,6 +288,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   auto steps = [&](auto nl) {
     constexpr int NL = decltype(nl)::value;
     constexpr int kReads = NL + MT, kProducts = MT * NL;
+    // The checkpoint's scales are float32 outputs, and a long chain of joins shows
+    // in them (K = 2048: 2.5e-7 of a value against a library product's 1.1e-7).
+    // So the sums of 128 columns (narrow tile, bound by the weights' stream) or
+    // 512 (middle tile) join a total; the large tile has no registers for one.
+    constexpr int kJoin = EPI != Epi::kUp ? 0 : BN <= 32 ? 2 : BN <= 128 ? 8 : 0;   // steps
+    v4f total[kJoin ? MT : 1][kJoin && NL > 0 ? NL : 1] = {};
     v8bf a[2][MT], b[2][NL > 0 ? NL : 1];
     auto read = [&](int kb, int kh, int i) {   // the i-th operand of a half
       if (i < NL) b[kh][i] = rr.load(lds_r + (kb % SR) * kRight, i * WN + wn, kh);
@@ -308,6 +332,17 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
         else if (i - r0 < LL && left) issue_left(kb + SL, i - r0);
         else issue_right(kb + SR, i - r0 - (left ? LL : 0));
       });
+      if constexpr (kJoin && NL > 0) {
+        if ((kb + 1) % kJoin == 0) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+              total[m][j] += acc[m][j];
+              acc[m][j] = v4f{0, 0, 0, 0};
+            }
+        }
+      }
     };
     if (KB == 0) return;
     arrived(0);
@@ -320,6 +355,12 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
     for (; kb + SL < KB; ++kb) step(kb, std::true_type(), std::true_type(), std::false_type());
     for (; kb + 1 < KB; ++kb) step(kb, std::true_type(), std::false_type(), std::false_type());
     step(kb, std::false_type(), std::false_type(), std::false_type());
+    if constexpr (kJoin && NL > 0) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NL; ++j) acc[m][j] += total[m][j];
+    }
   };
   // A loop for each number of live tiles.
   auto pick = [&](auto self, auto nl) -> void {
@@ -517,24 +558,62 @@ int launch_rows(ProductArgs A, int64_t slots, int cus, hipStream_t st) {
   const int64_t tiles = (slots / A.bn + active) * nf;   // no fewer than the rows can need
   const int64_t grid = (tiles + 7) / 8 * 8;
   if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
-  const auto k = A.E <= 4 * kWave ? k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 4>
-                                  : k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 16>;
+  auto k = k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 4>;   // the small tile: at most 256 experts
+  if constexpr (BM > 128)
+    if (A.E > 4 * kWave) k = k_ffn_product<EPI, LC, BM, BN, WM, WN, SL, SR, 16>;
   return launch("k_ffn_product", k, dim3((uint32_t)grid), dim3(kThreadsHere), 0, st, A);
 }
 
+// The tile goes by the rows that an active expert has on average, all that the
+// host knows of the load.  us of each tile; "even": 32 experts, "Zipf": 64 experts,
+// a few with most of the rows; H = 7168, I = 2048; up / down / up gradient /
+// transposed.
+//   - narrow, 32 rows in workgroups of 4 waves, up to 24 rows an expert:
+//       even    24                    32                    48
+//       narrow  314 179 165 330       340 194 200 378       390 226 192 394
+//       middle  316 181 173 334       319 173 219 338       324 216 221 344
+//       Zipf    16                    32                    64
+//       narrow  583 323 322 615       732 389 393 755       1037 528 527 1030
+//       middle  584 320 323 589       687 343 410 664       708 395 414 719
+//   - middle, 128 rows and three stages of both operands;
+//   - small, 128 features x 128 rows, where the middle tile would leave half of the
+//     compute units without one (one expert; up gradient, down):
+//       rows    200        500        1000       1337       2000
+//       small   41 14      43 19      48         53         63
+//       middle  67 19      68 22      70         76         80
+//     (down with 1000 rows, 224 middle tiles: 34 against 29.)  Up's tile cannot
+//     shrink, it holds a gate and an up block of 128 features;
+//   - large, 256 rows, above 150 rows an expert where there are two tiles for every
+//     compute unit at least (200 rows, up gradient with one: 377 against 283):
+//       even    128           160           200           256
+//       middle  429 248 455   483 273 493   516 266 526   631 317 634   (up, down, transposed)
+//       large   394 259 425   410 266 441   445 242 472   566 302 619
+//       Zipf    128               170                 256                 400
+//       middle  904 452 533 894   1071 512 578 1009   1340 653 756 1307   1878 916 1046 1825
+//       large   991 458 557 918   1038 517 574 1026   1248 619 745 1259   1666 820  976 1670
 template <Epi EPI, bool LC>
 int launch_any(const ProductArgs& A, int64_t slots, int cus, hipStream_t st) {
   constexpr int BF = EPI == Epi::kUp ? 128 : 256;
-  const int64_t active = slots < A.E ? slots : A.E, avg = slots / active;
-  const int64_t big = active * ((avg + 255) / 256) * ((A.F + BF - 1) / BF);   // tiles of 256 rows
-  if (avg > 256 && big >= 2 * cus) return launch_rows<EPI, LC, 256, 256, 2, 4, 2, LC ? 2 : 3>(A, slots, cus, st);
-  if (avg > 48) return launch_rows<EPI, LC, 256, 128, 4, 2, 3, 3>(A, slots, cus, st);
+  const int64_t active = slots < A.E ? slots : A.E, avg = slots / active, nf = (A.F + BF - 1) / BF;
+  // The third stage of the right operand pays where both lie in rows (up: 3.39
+  // ms against 3.55, the transposed product 3.32 against 3.24).
+  if (avg > 150 && active * ((avg + 255) / 256) * nf >= 2 * cus)
+    return launch_rows<EPI, LC, 256, 256, 2, 4, 2, LC ? 2 : 3>(A, slots, cus, st);
+  if (avg > 24) {
+    if constexpr (EPI != Epi::kUp) {
+      if (2 * active * ((avg + 127) / 128) * nf <= cus && A.E <= 4 * kWave)
+        return launch_rows<EPI, LC, 128, 128, 2, 4, 4, 4>(A, slots, cus, st);
+    }
+    return launch_rows<EPI, LC, 256, 128, 4, 2, 3, 3>(A, slots, cus, st);
+  }
   return launch_rows<EPI, LC, 256, 32, 4, 1, 3, 3>(A, slots, cus, st);
 }
 
-template <int BM, int BN, int WM, int WN>
+// One tile of 256 x 256 for every load: with tiles of 128 x 128, two workgroups on a
+// compute unit, 5 rows an expert took 628 us against 507, 2048 rows 5.05 ms against
+// 3.56.
 int launch_wgrad(const ProductArgs& A, hipStream_t st) {
-  constexpr int kThreadsHere = WM * WN * kWave;
+  constexpr int BM = 256, BN = 256, WM = 2, WN = 4, kThreadsHere = WM * WN * kWave;
   const int64_t per = (int64_t)((A.F + BM - 1) / BM) * ((A.G + BN - 1) / BN), grid = (per + 7) / 8 * 8 * A.E;
   if (grid * kThreadsHere > UINT32_MAX) return MOE_ERANGE;
   return launch("k_ffn_product", k_ffn_product<Epi::kWgrad, true, BM, BN, WM, WN, 2, 2, 1>, dim3((uint32_t)grid),
@@ -590,7 +669,7 @@ int launch_grouped_wgrad(const Dims& D, const uint16_t* d, const uint16_t* x, co
   A.G = F;
   A.f32 = f32;
   A.add = add;
-  return launch_wgrad<256, 256, 2, 4>(A, st);
+  return launch_wgrad(A, st);
 }
 
 }  // namespace moe

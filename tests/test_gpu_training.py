@@ -108,6 +108,11 @@ def run_products(N, E, counts, H, I, T, k, R_=0, seed=1, flags=True):  # noqa: E
     (2, 4, 513, 2, 2048, 384),
     (2, 8, 2000, 2, 384, 4096),         # enough tiles of 256 rows: the large tile
     (1, 320, 3000, 1, 128, 128),        # more than 256 experts, uneven
+    (4, 64, 400, 4, 1024, 640),         # the middle tile on every side
+    (1, 320, 30000, 1, 128, 128),       # the same with more than 256 experts
+    (2, 32, 2500, 2, 2048, 256),        # the large tile for the products of rows and of columns
+    (2, 32, 2500, 2, 256, 2048),        # and for the up product's gradient
+    (4, 512, 25600, 1, 128, 128),       # the same with more than 256 experts
 ])
 def test_products_shapes(N, E, T, k, H, I):  # noqa: E741
     log(f"products N={N} E={E} T={T} k={k} H={H} I={I}")
@@ -398,6 +403,20 @@ def test_block_norm_parts():
     check_norm(sh, x, res, gp, gate, 0.0, gn)
     assert (check_norm_grad(sh, dy, dr, x, res, gp, gate, 0.0, gn)["dresidual"] == 0).all()
     check_norm_grad(sh, dy, dr, x, res, gp, torch.zeros_like(gate), 1.0, gn)
+
+
+def test_block_norm_grad_where_the_terms_cancel():
+    """residual = -gate * (x / rms(x) * gamma_post) but for a bf16 rounding and a
+    few columns: r is small beside both of its terms."""
+    log("block norm cancelling")
+    N, T, H = 2, 9, 1024
+    sh, x, res, gp, gate, gn, dy, dr = norm_case(N, T, H, 3)
+    x = normal((N, T, H), gen(4))
+    n1 = x.double() / torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + 1e-5) * gp.double()
+    res = (-gate.double()[..., None] * n1).to(BF)
+    res[..., :8] = 0
+    check_norm(sh, x, res, gp, gate, 1.0, gn)
+    check_norm_grad(sh, dy, dr, x, res, gp, gate, 1.0, gn)
 
 
 def test_block_norm_values():
