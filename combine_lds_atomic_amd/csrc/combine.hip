@@ -643,7 +643,7 @@ __global__ __launch_bounds__(WAVES* kWave) void k_comb_grad(Dims D, Ws W, const 
       }
     }
     if (dw) {
-      if (WAVES > 1) __syncthreads();
+      __syncthreads();
       if ((int)threadIdx.x < D.k) {
         float s = 0.0f;
 #pragma unroll

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   constexpr int LPS = LL + LR;
   static_assert(LL * NW * 1024 == BM * kStepBytes && LR * NW * 1024 == BN * kStepBytes, "loads split evenly");
   static_assert(MT % (EPI == Epi::kUp ? 4 : 2) == 0, "the epilogue takes tiles in pairs");
-  static_assert(EPI != Epi::kUp || BM == 2 * kScaleBlock, "a gate and an up half of one scale block");
+  static_assert(EPI != Epi::kUp || (BM == 2 * kScaleBlock && LL % 2 == 0), "a gate and an up half of one scale block");
   static_assert(SR == SL || SR == SL + 1, "the right operand's loads are a step's last");
   constexpr int kLeft = BM * kStepBytes, kRight = BN * kStepBytes;   // bytes of a stage
   __shared__ __align__(1024) unsigned char lds[SL * kLeft + SR * kRight];
@@ -198,9 +198,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   for (int i = 0; i < LL; ++i) {
     if constexpr (LC) {
       loff[i] = col_off(BM, i, ft * BM, A.F) + (RC ? 0u : (uint32_t)col_row(BM, i) * (uint32_t)A.F * 2u);
-    } else if constexpr (EPI == Epi::kUp) {
-      const int r = i * NW * 8 + (int)r0;
-      loff[i] = (uint32_t)(r < BF ? r : A.F + r - BF) * (uint32_t)A.K * 2u + c0;   // F * K <= 2^30
+    } else if constexpr (EPI == Epi::kUp) {   // the second half of the loads: up rows, F rows on
+      loff[i] = (uint32_t)((i % (LL / 2)) * NW * 8 + r0) * (uint32_t)A.K * 2u + c0;
     } else {
       loff[i] = min(i * NW * 8 + r0, (uint32_t)(A.F - ft * BF) - 1u) * (uint32_t)A.K * 2u + c0;
     }
@@ -218,7 +217,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
     } else if constexpr (LC) {
       load_lds16(lbase + (int64_t)kb * kBK * A.F, loff[i], dst);
     } else {
-      load_lds16(lbase + kb * kBK, loff[i], dst);
+      const int64_t up = EPI == Epi::kUp && i >= LL / 2 ? (int64_t)A.F * A.K : 0;
+      load_lds16(lbase + up + kb * kBK, loff[i], dst);
     }
   };
   auto issue_right = [&](int kb, int i) {

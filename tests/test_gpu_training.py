@@ -246,6 +246,29 @@ def test_products_offsets_beyond_32_bits():
     assert (w[:2] == 0).all()
 
 
+def test_up_largest_features():
+    """The largest K and I: an expert's up rows lie 2^31 bytes behind its gate rows."""
+    log("up, largest features")
+    g, n, K = gen(11), 5, 32768
+    sh, eo = moe.shape(1, n, 128, 1, 1), make_groups(1, 1, [n])
+    w13 = torch.zeros((1, 2 * K, K), dtype=BF, device="cuda")
+    for f in (0, K - 128, K, 2 * K - 128):
+        w13[0, f:f + 128] = normal((128, K), g, K ** -0.5)
+    x = normal((n, K), g)
+    a = torch.empty((n, K), dtype=BF, device="cuda")
+    q, s = torch.empty((n, 2 * K), dtype=torch.uint8, device="cuda"), torch.empty((n, 2 * K // 128), device="cuda")
+    moe.moe_ffn_up(sh, x, w13, eo, K, K, a, q, s)
+    for f in (0, K - 128):
+        part = torch.cat((w13[0, f:f + 128], w13[0, K + f:K + f + 128]))
+        av, ab, hv, hb = R.up(x, part)
+        R.check_bf16(a[:, f:f + 128], av, ab, f"a from {f}")
+        for half in (0, 1):
+            c = slice(half * K + f, half * K + f + 128)
+            h = slice(half * 128, half * 128 + 128)
+            X.check_quantised(q[:, c].contiguous(), s[:, c.start // 128:c.start // 128 + 1], hv[:, h], hb[:, h])
+    assert (a[:, 128:K - 128] == 0).all()
+
+
 # ------------------------------------------------------------------ combine
 
 def routed(N, T, E, k, H, seed, R_=0, bad=False, early=0):
