@@ -69,25 +69,19 @@ __device__ __forceinline__ v4u unit(const uint16_t* p, int64_t at, int c) {
 // Keeps the compiler from holding what it unpacked from `v` for the next use.
 __device__ __forceinline__ void forget(v4u& v) { asm volatile("" : "+v"(v)); }
 
-// Sums of V values over the threads of a row, the same in all of them.  A
-// barrier lies between one use of `part` and the next.
-template <int V, bool WAVE>
-__device__ __forceinline__ void row_sum(float (&v)[V], float (*part)[V]) {
+// v's sum over the threads of a row, the same in all of them.  A barrier lies
+// between one use of `part` and the next.
+template <bool WAVE>
+__device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1)
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += __shfl_xor(v[i], d);
+  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
   if constexpr (!WAVE) {
-    if ((threadIdx.x & (kWave - 1)) == 0)
-#pragma unroll
-      for (int i = 0; i < V; ++i) part[threadIdx.x / kWave][i] = v[i];
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.0f;
-    for (int w = 0; w < (int)blockDim.x / kWave; ++w)
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += part[w][i];
+    v = 0.0f;
+    for (int w = 0; w < (int)blockDim.x / kWave; ++w) v += part[w];
   }
+  return v;
 }
 
 // v's value from the lane that DPP control `Ctrl` names, added.
@@ -135,9 +129,12 @@ __device__ __forceinline__ void row_sum8(float (&v)[8], float (*part)[8]) {
 // wave per row if WAVE (no barrier), otherwise a workgroup.  Every read of a
 // row comes before the first write to it, so outputs may be the inputs' own
 // memory.
+//
+// Bound by HBM: 8 H bytes a row, 622 to 651 us for 65536 rows of 7168 (5.8 to
+// 6.0 TB/s, where a plain copy reaches 6.7); one token takes 4 us.
 template <int U, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(BlockArgs A) {
-  __shared__ float p1[kMaxWaves][1], p2[kMaxWaves][1];
+  __shared__ float p1[kMaxWaves], p2[kMaxWaves];
   const int threads = WAVE ? kWave : blockDim.x;
   const int tid = WAVE ? (threadIdx.x & (kWave - 1)) : threadIdx.x;
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + threadIdx.x / kWave : blockIdx.x;
@@ -145,7 +142,7 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
   const int units = A.H / 8;
   const int64_t at = row * A.H;
   const float gate = A.gate ? A.gate[row] : 1.0f;
-  float x[U][8], r[U][8], s1[1] = {0.0f}, s2[1] = {0.0f};
+  float x[U][8], r[U][8], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = tid + u * threads;
@@ -157,10 +154,10 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
     unpack8(a, x[u]);
     unpack8(b, r[u]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s1[0] = __builtin_fmaf(x[u][i], x[u][i], s1[0]);
+    for (int i = 0; i < 8; ++i) s1 = __builtin_fmaf(x[u][i], x[u][i], s1);
   }
-  row_sum<1, WAVE>(s1, p1);
-  const float i1 = 1.0f / sqrtf(s1[0] / (float)A.H + A.eps);
+  s1 = row_sum<WAVE>(s1, p1);
+  const float i1 = 1.0f / sqrtf(s1 / (float)A.H + A.eps);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = tid + u * threads;
@@ -169,13 +166,13 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       r[u][i] = A.alpha * r[u][i] + gate * (x[u][i] * i1 * g[i]);
-      s2[0] = __builtin_fmaf(r[u][i], r[u][i], s2[0]);
+      s2 = __builtin_fmaf(r[u][i], r[u][i], s2);
     }
     if (c < units) st16(reinterpret_cast<v4u*>(A.o0 + at) + c, pack8(r[u]));
   }
   if (!A.o1) return;
-  row_sum<1, WAVE>(s2, p2);
-  const float i2 = 1.0f / sqrtf(s2[0] / (float)A.H + A.eps);
+  s2 = row_sum<WAVE>(s2, p2);
+  const float i2 = 1.0f / sqrtf(s2 / (float)A.H + A.eps);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = tid + u * threads;
@@ -190,71 +187,106 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 
 // Backwards: a workgroup takes rows blockIdx.x, + gridDim.x, ... and keeps its
 // columns' sums of the two dgammas in registers until the last of them.  With
-// AHEAD the next row's loads are issued before this one is worked on.
+// KEEP a row stays in registers between its reduction and its outputs, and the
+// next row's loads are issued before this one is worked on; without, both are
+// too large for the registers and the row is read again.
 //
 // r is linear in 1 / rms(x), so one reduction of seven sums gives both roots,
 // the part of t along r and dgate, where a reduction after each of them would
 // be three.  The sum of r^2 comes out of its three parts; where the residual
 // and the block's term cancel to less than an eighth of those, it is formed
 // from r itself in a second reduction.
-template <int U, bool AHEAD>
+//
+// Bound by HBM and, nearly as much, by its 350 vector instructions a wave and
+// row: 1001 to 1097 us for 65536 rows of 7168 (12 H bytes a row, 5.1 to 5.6
+// TB/s).  One unit a thread leaves registers for the next row's loads; two
+// units took 1146, three reductions a row 1184, and 2 workgroups a compute
+// unit without loads ahead 2.4 ms, since registers went to scratch.  Rows above 8192
+// are read twice (958 us at 32768 rows of 8320, 1270 with all of it in registers
+// and scratch); at H = 32768, with 1.3 TB/s before one of the sums went to LDS and
+// 2.1 since, some registers still go to scratch.
+template <int U, bool KEEP>
 __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
-  __shared__ float part[2][kMaxWaves][8], one[kMaxWaves][1];
+  __shared__ float part[2][kMaxWaves][8], one[kMaxWaves];
   const int threads = blockDim.x, units = A.H / 8;
   const v4u zero = {0, 0, 0, 0};
   const float h = 1.0f / (float)A.H;
-  float dgp[U][8], dgn[U][8];
-  v4u gp[U], gn[U];
+  // With four units one of the two sums is in LDS, each thread's own, else in registers.
+  constexpr bool kLds = U > 2;
+  __shared__ float4 lds_sum[kLds ? U * kMaxThreads * 2 : 1];
+  float dgp[kLds ? 1 : U][8], dgn[U][8];
+  v4u gp[KEEP ? U : 1], gn[KEEP ? U : 1];
+  auto gammas = [&](int u) {
+    const int c = threadIdx.x + u * threads;
+    gp[KEEP ? u : 0] = c < units ? *(reinterpret_cast<const v4u*>(A.gamma_post) + c) : zero;
+    gn[KEEP ? u : 0] = c < units && A.gamma_next ? *(reinterpret_cast<const v4u*>(A.gamma_next) + c) : zero;
+  };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = threadIdx.x + u * threads;
-    gp[u] = c < units ? *(reinterpret_cast<const v4u*>(A.gamma_post) + c) : zero;
-    gn[u] = c < units && A.gamma_next ? *(reinterpret_cast<const v4u*>(A.gamma_next) + c) : zero;
+    if constexpr (KEEP) gammas(u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dgp[u][i] = dgn[u][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) dgp[kLds ? 0 : u][i] = dgn[u][i] = 0.0f;
+    if constexpr (kLds)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lds_sum[(u * kMaxThreads + threadIdx.x) * 2 + i] = float4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   struct Row {
-    v4u x[U], r[U], t[U], d[U];
+    v4u x[KEEP ? U : 1], r[KEEP ? U : 1], t[KEEP ? U : 1], d[KEEP ? U : 1];
   };
-  auto read = [&](int64_t row, Row& q) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = threadIdx.x + u * threads;
-      const bool in = c < units;
-      q.x[u] = in ? unit(A.x, row * A.H, c) : zero;
-      q.r[u] = in ? unit(A.residual, row * A.H, c) : zero;
-      q.t[u] = in && A.dy ? unit(A.dy, row * A.H, c) : zero;
-      q.d[u] = in && A.dr ? unit(A.dr, row * A.H, c) : zero;
-    }
+  auto read = [&](int64_t row, int u, Row& q) {
+    const int c = threadIdx.x + u * threads, i = KEEP ? u : 0;
+    const bool in = c < units;
+    auto get = [&](const uint16_t* p) {   // what is read twice may stay in the caches
+      return KEEP ? unit(p, row * A.H, c) : *(reinterpret_cast<const v4u*>(p + row * A.H) + c);
+    };
+    q.x[i] = in ? get(A.x) : zero;
+    q.r[i] = in ? get(A.residual) : zero;
+    q.t[i] = in && A.dy ? get(A.dy) : zero;
+    q.d[i] = in && A.dr ? get(A.dr) : zero;
   };
   Row next;
-  if (AHEAD && blockIdx.x < A.rows) read(blockIdx.x, next);
+  if (KEEP && blockIdx.x < A.rows)
+#pragma unroll
+    for (int u = 0; u < U; ++u) read(blockIdx.x, u, next);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
     const int64_t at = row * A.H;
     const float gate = A.gate ? A.gate[row] : 1.0f;
     Row q;
-    if constexpr (AHEAD) {
+    if constexpr (KEEP) {
       q = next;
-      if (row + gridDim.x < A.rows) read(row + gridDim.x, next);
-    } else {
-      read(row, q);
+      if (row + gridDim.x < A.rows)
+#pragma unroll
+        for (int u = 0; u < U; ++u) read(row + gridDim.x, u, next);
     }
+    // What a unit needs, from the registers or again from memory.
+    auto bring = [&](int u) {
+      if constexpr (KEEP) {
+        forget(q.x[u]);
+        forget(q.r[u]);
+        forget(q.t[u]);
+        forget(q.d[u]);
+        forget(gp[u]);
+        forget(gn[u]);
+      } else {
+        read(row, u, q);
+        gammas(u);
+      }
+    };
     // sums of: x x, (x gp)^2, res res, res x gp, t res, t x gp, dr x gp
     float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      forget(gp[u]);
-      forget(gn[u]);
+      bring(u);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float x[4], r[4], g[4], n[4], t[4], d[4];
-        unpack4(q.x[u], half, x);
-        unpack4(q.r[u], half, r);
-        unpack4(gp[u], half, g);
-        unpack4(gn[u], half, n);
-        unpack4(q.t[u], half, t);
-        unpack4(q.d[u], half, d);
+        unpack4(q.x[KEEP ? u : 0], half, x);
+        unpack4(q.r[KEEP ? u : 0], half, r);
+        unpack4(gp[KEEP ? u : 0], half, g);
+        unpack4(gn[KEEP ? u : 0], half, n);
+        unpack4(q.t[KEEP ? u : 0], half, t);
+        unpack4(q.d[KEEP ? u : 0], half, d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float xg = x[i] * g[i], tn = t[i] * n[i];
@@ -274,21 +306,21 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
     const float apart = A.alpha * A.alpha * m[2] + b * b * m[1];
     float rr = apart + 2.0f * A.alpha * b * m[3];
     if (!(rr >= 0.125f * apart)) {   // the residual and the block nearly cancel: the sum of r itself
-      float v[1] = {0.0f};
+      float v = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        bring(u);
         float x[8], r[8], g[8];
-        unpack8(q.x[u], x);
-        unpack8(q.r[u], r);
-        unpack8(gp[u], g);
+        unpack8(q.x[KEEP ? u : 0], x);
+        unpack8(q.r[KEEP ? u : 0], r);
+        unpack8(gp[KEEP ? u : 0], g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float w = A.alpha * r[i] + b * (x[i] * g[i]);
-          v[0] = __builtin_fmaf(w, w, v[0]);
+          v = __builtin_fmaf(w, w, v);
         }
       }
-      row_sum<1, false>(v, one);
-      rr = v[0];
+      rr = row_sum<false>(v, one);
     }
     const float i2 = rsqrtf(rr * h + A.eps);
     const float along = (A.alpha * m[4] + b * m[5]) * h * i2 * i2;
@@ -298,34 +330,33 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = threadIdx.x + u * threads;
-      forget(q.x[u]);
-      forget(q.r[u]);
-      forget(q.t[u]);
-      forget(q.d[u]);
-      forget(gp[u]);
-      forget(gn[u]);
+      bring(u);
       v4u dx, dres;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float x[4], r[4], g[4], n[4], t[4], d[4];
-        unpack4(q.x[u], half, x);
-        unpack4(q.r[u], half, r);
-        unpack4(gp[u], half, g);
-        unpack4(gn[u], half, n);
-        unpack4(q.t[u], half, t);
-        unpack4(q.d[u], half, d);
+        unpack4(q.x[KEEP ? u : 0], half, x);
+        unpack4(q.r[KEEP ? u : 0], half, r);
+        unpack4(gp[KEEP ? u : 0], half, g);
+        unpack4(gn[KEEP ? u : 0], half, n);
+        unpack4(q.t[KEEP ? u : 0], half, t);
+        unpack4(q.d[KEEP ? u : 0], half, d);
+        float sum[4];
+        float4* mine = &lds_sum[kLds ? (u * kMaxThreads + threadIdx.x) * 2 + half : 0];
+        if constexpr (kLds) *reinterpret_cast<float4*>(sum) = *mine;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           r[i] = A.alpha * r[i] + b * (x[i] * g[i]);
           d[i] = d[i] + i2 * (t[i] * n[i]) - k1 * r[i];
           float& gn_sum = dgn[u][half * 4 + i];
-          float& gp_sum = dgp[u][half * 4 + i];
+          float& gp_sum = kLds ? sum[i] : dgp[kLds ? 0 : u][half * 4 + i];
           gn_sum = __builtin_fmaf(t[i], r[i] * i2, gn_sum);
           const float e = b * d[i];
           gp_sum = __builtin_fmaf(e, x[i], gp_sum);
           x[i] = e * g[i] - x[i] * k0;
           d[i] *= A.alpha;
         }
+        if constexpr (kLds) *mine = *reinterpret_cast<float4*>(sum);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           dx[2 * half + i] = cvt_bf16(x[2 * i], x[2 * i + 1]);
@@ -346,7 +377,10 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
     if (c >= units) continue;
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      *reinterpret_cast<float4*>(out + c * 8 + i) = float4{dgp[u][i], dgp[u][i + 1], dgp[u][i + 2], dgp[u][i + 3]};
+      if constexpr (kLds)
+        *reinterpret_cast<float4*>(out + c * 8 + i) = lds_sum[(u * kMaxThreads + threadIdx.x) * 2 + i / 4];
+      else
+        *reinterpret_cast<float4*>(out + c * 8 + i) = float4{dgp[u][i], dgp[u][i + 1], dgp[u][i + 2], dgp[u][i + 3]};
       *reinterpret_cast<float4*>(out + A.H + c * 8 + i) = float4{dgn[u][i], dgn[u][i + 1], dgn[u][i + 2], dgn[u][i + 3]};
     }
   }
@@ -382,8 +416,8 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void k_block_norm_join(const flo
   if (out) out[c < H ? c : c - H] = s;
 }
 
-// Units of a thread backwards: the fewest that leave a workgroup of at most
-// 1024 threads.  With two or four, registers are short and some go to scratch.
+// Units of a thread backwards: the fewest that leave a workgroup of at most 1024
+// threads.
 inline int grad_units(int H) { return H <= 8 * kMaxThreads ? 1 : H <= 16 * kMaxThreads ? 2 : 4; }
 inline int grad_threads(int H) {
   const int u = grad_units(H);

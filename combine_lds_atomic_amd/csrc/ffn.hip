@@ -116,20 +116,25 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
 // the operands sit in LDS, filled by loads that bypass the registers.
 //
 // What bounds it on MI355X (2048 rows for each of 32 experts, H = 7168, I =
-// 2048, runs on four machines): up 3.30 to 3.39 ms (1.14 to 1.17 PFLOP/s), down 1.65
-// to 1.72, the transposed product 3.12 to 3.32 (1.16 to 1.23), up gradient 1.88
-// to 1.96 (0.98 to 1.02), weight gradients 3.23 and 1.58 (1.19 to 1.22); large
-// library products of the three layouts reach 1.60 (rows x rows), 1.38 and 1.18.
-// The matrix pipes are busy 54% to 61% of the cycles at a clock that falls to
-// 1.9 GHz; LDS reads have no bank conflicts.  A timing copy whose loads stay on
-// two steps (so in L2) took 3.00 ms against 3.57 for up and 3.02 against 3.33
-// transposed, one without the loop's loads 2.68 and 2.66; so a sixth of the time is
-// the way to memory, and deeper stages are what helped (a 256 x 128 tile with three
-// stages against two: 3.99 ms against 4.85).  An epilogue is 128 to 512 KiB a
-// tile that all compute units write at the same time.  Tried and slower: four
-// waves of 128 x 128 (3.9 to 4.4 ms up, whatever the order of its reads), steps of 32
-// columns with four or five stages (3.70), non-temporal stores of y (down
-// 1.72 against 1.65) and of weight gradients (3.46 against 3.32).
+// 2048; ranges are over machines and runs): up 3.25 to 3.43 ms (1.12 to 1.18
+// PFLOP/s), down 1.65 to 1.73, the transposed product 3.11 to 3.24 (1.19 to 1.24), up
+// gradient 1.87 to 1.95 (0.99 to 1.03), weight gradients 3.21 to 3.33 and 1.55 to
+// 1.60 (1.16 to 1.24); large library products of the three layouts reach 1.60 (rows
+// x rows), 1.38 and 1.18.  The matrix pipes are busy 51% to 64% of the cycles
+// at a clock that falls to 1.77 to 1.9 GHz; LDS reads have no bank conflicts.
+// Timing copies: with loads that stay on two steps (so in L2) 3.00 ms for up and 3.02
+// transposed, against 3.57 and 3.33 then; without the loop's loads 2.68 and 2.66;
+// without the epilogue 3.05, 1.42, 2.94, 1.58, 2.82 and 1.43 (so the 128 to 512 KiB
+// that all compute units write at about the same time cost 7% to 16%).  Deeper
+// stages are what helped most: a 256 x 128 tile with three stages against two took
+// 3.99 ms against 4.85.
+// Tried and slower: four waves of 128 x 128 (up 3.9 to 4.4 ms, whatever the order of
+// its reads); steps of 32 columns with four or five stages (3.70); 32 x 32 matrix
+// instructions (3% to 5%); groups of 2 to 6 token tiles (up to 9%); non-temporal
+// stores of y (down 1.72 against 1.65) and of weight gradients (3.46 against 3.32);
+// workgroups that take tile after tile and load the next one's first stages before
+// they store (down 1.75 against 1.65; weight gradients of 5 rows an expert 747 us
+// against 520: finding the next tile is in the way of a short one).
 template <Epi EPI, bool LC, int BM, int BN, int WM, int WN, int SL, int SR, int EPL>
 __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   constexpr bool RC = EPI == Epi::kWgrad;
