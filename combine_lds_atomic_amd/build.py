@@ -1,8 +1,8 @@
 """Build libmoe_ep.so and libmoe_streams.so (HIP, gfx950) in-tree with hipcc.
 
 Each .hip source is compiled to an object in parallel, then linked into
-``combine_lds_atomic_amd/libmoe_ep.so`` (dispatch / combine and the expert
-layer, include/moe_ep.h)
+``combine_lds_atomic_amd/libmoe_ep.so`` (dispatch / combine, the expert layer
+and its training, include/moe_ep.h)
 and ``combine_lds_atomic_amd/libmoe_streams.so`` (the benchmark's plain
 streams, include/moe_streams.h).  Usage: ``python
 combine_lds_atomic_amd/build.py`` (or ``__graft_entry__.build()``); run it by

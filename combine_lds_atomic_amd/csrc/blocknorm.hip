@@ -381,7 +381,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
         *reinterpret_cast<float4*>(out + c * 8 + i) = lds_sum[(u * kMaxThreads + threadIdx.x) * 2 + i / 4];
       else
         *reinterpret_cast<float4*>(out + c * 8 + i) = float4{dgp[u][i], dgp[u][i + 1], dgp[u][i + 2], dgp[u][i + 3]};
-      *reinterpret_cast<float4*>(out + A.H + c * 8 + i) = float4{dgn[u][i], dgn[u][i + 1], dgn[u][i + 2], dgn[u][i + 3]};
+      *reinterpret_cast<float4*>(out + A.H + c * 8 + i) =
+          float4{dgn[u][i], dgn[u][i + 1], dgn[u][i + 2], dgn[u][i + 3]};
     }
   }
 }
@@ -496,12 +497,14 @@ int launch_block_norm_grad(const Dims& D, const uint16_t* dy, const uint16_t* dr
   const dim3 threads(grad_threads(D.H));
   if (groups) {
     const int u = grad_units(D.H);
-    const auto k = u == 1 ? k_block_norm_grad<1, true> : u == 2 ? k_block_norm_grad<2, false> : k_block_norm_grad<4, false>;
+    const auto k = u == 1   ? k_block_norm_grad<1, true>
+                   : u == 2 ? k_block_norm_grad<2, false>
+                            : k_block_norm_grad<4, false>;
     const int rc = launch("k_block_norm_grad", k, dim3((uint32_t)groups), threads, 0, st, A);
     if (rc != MOE_OK) return rc;
   }
-  return launch("k_block_norm_join", k_block_norm_join, dim3(2 * D.H / kWave), dim3(kJoinWaves * kWave), 0, st, A.part, (int)groups,
-                D.H, dgamma_post, dgamma_next);
+  return launch("k_block_norm_join", k_block_norm_join, dim3(2 * D.H / kWave), dim3(kJoinWaves * kWave), 0, st, A.part,
+                (int)groups, D.H, dgamma_post, dgamma_next);
 }
 
 }  // namespace moe

@@ -549,9 +549,10 @@ __global__ __launch_bounds__(kPsThreads) void k_comb_send_partial(Dims D, Ws W, 
 //   dy[p] = bf16(w[s][t][j] * dout[s][t]),  dw[s][t][j] = <dout[s][t], y[p]>  (0 without a row).
 // One workgroup of WAVES waves per token.  A thread takes the 16-byte units
 // threadIdx, + 64 WAVES, ... of a row, U of them at a time (all of them if ONE:
-// dout is then read once), and G slots' units are on their way together.  Lane j of every wave looks slot j's row up (k is at most 64), so
-// the routing tables are read once for all slots.  y (and dw) or dy may be null, or
-// the same memory; without weights (w null) every weight is 1.
+// dout is then read once), and G slots' units are on their way together.  Lane
+// j of every wave looks slot j's row up (k is at most 64), so the routing tables
+// are read once for all slots.  y (and dw) or dy may be null, or the same
+// memory; without weights (w null) every weight is 1.
 //
 // Bound by HBM: rows of two arrays read and written in the order of the
 // routing, 3.11 ms for 65536 tokens, 524288 rows of 7168 (16.0 GB: 5.1 TB/s,
@@ -715,8 +716,8 @@ int launch_comb_grad(const Dims& D, const Ws& W, const uint16_t* dout, const uin
   const int rc = launch("k_comb_grad", k, dim3(os_grid(tokens, 1)), dim3(waves * kWave), 0, st, D, W, dout, y, idx,
                         send_pos, w, dy, dw);
   if (rc || !D.R || !dy) return rc;
-  return launch("k_comb_zero_holes", k_comb_zero_holes, dim3((uint32_t)std::min<int64_t>((D.rows + kThreads - 1) / kThreads, 4096)),
-                dim3(kThreads), 0, st, D, W, row_src, dy);
+  const int groups = std::min((D.rows + kThreads - 1) / kThreads, 4096);
+  return launch("k_comb_zero_holes", k_comb_zero_holes, dim3(groups), dim3(kThreads), 0, st, D, W, row_src, dy);
 }
 
 constexpr int64_t kPsMinTokens = 16384;   // tokens (N*T) from which the cooperative form is used

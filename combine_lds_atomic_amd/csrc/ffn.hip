@@ -107,7 +107,7 @@ struct Reader {
   }
 };
 
-// 1 / (1 + exp(-g)); the reciprocal instruction is off by one unit in the last place.
+// 1 / (1 + exp(-g)); the reciprocal instruction is off by at most one unit in the last place.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // One workgroup forms BM left features x up to BN right rows of one expert:
@@ -147,6 +147,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   static_assert(EPI != Epi::kUp || (BM == 2 * kScaleBlock && LL % 2 == 0), "a gate and an up half of one scale block");
   static_assert(SR == SL || SR == SL + 1, "the right operand's loads are a step's last");
   constexpr int kLeft = BM * kStepBytes, kRight = BN * kStepBytes;   // bytes of a stage
+  static_assert(EPI != Epi::kUp || 2 * WM * BN * 4 + BN * 256 <= SL * kLeft + SR * kRight, "the epilogue's rows fit");
   __shared__ __align__(1024) unsigned char lds[SL * kLeft + SR * kRight];
   unsigned char* const lds_r = lds + SL * kLeft;
 

@@ -61,8 +61,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 // The same in one instruction (v_cvt_pk_bf16_f32), where the software rounding's
-// seven for each value would show; equal for every float but that a NaN keeps
-// its top payload bits.
+// seven for each value would show; the same bits for every float (all 2^32
+// compared) but that a NaN may be another NaN.
 __device__ __forceinline__ uint32_t cvt_bf16(float a, float b) {
   typedef float v2f __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));

@@ -471,8 +471,9 @@ int moe_layer_ll(const moe_shape *shape, const uint16_t *tokens, const int32_t *
  *
  * Row rules of the products, as for moe_grouped_gemm: exp_off int32
  * [N][E/N+1] from dispatch; rows that it gives to no expert are neither read
- * nor written; the shape's H must be valid but changes nothing.  Sums are
- * float32, products of bf16 exact.
+ * nor written; the shape's H must be valid but changes nothing; a shape whose
+ * tiles do not fit one launch is MOE_ERANGE.  Sums are float32, products of
+ * bf16 exact.
  */
 
 /*
