@@ -597,13 +597,24 @@ int launch_rows(ProductArgs A, int64_t slots, int cus, hipStream_t st) {
 //       Zipf    128               170                 256                 400
 //       middle  904 452 533 894   1071 512 578 1009   1340 653 756 1307   1878 916 1046 1825
 //       large   991 458 557 918   1038 517 574 1026   1248 619 745 1259   1666 820  976 1670
+//     A single expert's rows are known to the host, so its tile is chosen by the
+//     rounds that tiles of up to 128 and up to 256 rows need (up, down, up gradient,
+//     transposed):
+//       rows    1000              1337              2000               2300              4000
+//       middle  75 31  70  60     85 50  76  97     107 62 81  117     159 64 87  124    212 122 115 232
+//       large   90 32 100  63     95 40 101  75     111 49 104  92     125 53 110  98    172  98 123 182
 template <Epi EPI, bool LC>
 int launch_any(const ProductArgs& A, int64_t slots, int cus, hipStream_t st) {
   constexpr int BF = EPI == Epi::kUp ? 128 : 256;
   const int64_t active = slots < A.E ? slots : A.E, avg = slots / active, nf = (A.F + BF - 1) / BF;
   // The third stage of the right operand pays where both lie in rows (up: 3.39
   // ms against 3.55, the transposed product 3.32 against 3.24).
-  if (avg > 150 && active * ((avg + 255) / 256) * nf >= 2 * cus)
+  auto cost = [&](int BN) {   // rounds of tiles, as tile_rows prices them
+    const int bn = tile_rows(avg, active, (int)nf, BN, cus);
+    return (active * ((avg + bn - 1) / bn) * nf + cus - 1) / cus * (bn + 48);
+  };
+  if ((avg > 150 && active * ((avg + 255) / 256) * nf >= 2 * cus) ||
+      (A.E == 1 && avg > 24 && 9 * cost(256) < 8 * cost(128)))
     return launch_rows<EPI, LC, 256, 256, 2, 4, 2, LC ? 2 : 3>(A, slots, cus, st);
   if (avg > 24) {
     if constexpr (EPI != Epi::kUp) {

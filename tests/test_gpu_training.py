@@ -113,6 +113,8 @@ def run_products(N, E, counts, H, I, T, k, R_=0, seed=1, flags=True):  # noqa: E
     (2, 32, 2500, 2, 2048, 256),        # the large tile for the products of rows and of columns
     (2, 32, 2500, 2, 256, 2048),        # and for the up product's gradient
     (4, 512, 25600, 1, 128, 128),       # the same with more than 256 experts
+    (1, 1, 1337, 1, 6912, 256),         # one expert in one round of large tiles
+    (1, 1, 2300, 1, 256, 2048),         # and its up product
 ])
 def test_products_shapes(N, E, T, k, H, I):  # noqa: E741
     log(f"products N={N} E={E} T={T} k={k} H={H} I={I}")
