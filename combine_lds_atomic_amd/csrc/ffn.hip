@@ -54,7 +54,7 @@ __device__ __forceinline__ int expert_first(const ProductArgs& A, int e, int* n)
   const int lane = threadIdx.x & (kWave - 1), d = e / A.L;
   int off;
   *n = 0;
-  if (A.rows == 0) return 0;   // no tokens: exp_off is not there
+  if (A.rows == 0) return 0;   // no tokens: neither exp_off nor d and x are there
   *n = __builtin_amdgcn_readfirstlane(expert_rows(A, e, &off));
   if (A.R) return __builtin_amdgcn_readfirstlane(A.R * d + off);
   int before = 0;      // rows of the ranks in front
@@ -648,7 +648,7 @@ ProductArgs base_args(const Dims& D, const uint16_t* left, const uint16_t* right
   A.L = D.L;
   A.E = D.E;
   A.R = D.R;
-  A.rows = D.rows;
+  A.rows = D.T ? D.rows : 0;   // an empty batch has no rows, whatever its regions would hold
   A.K = K;
   A.F = F;
   return A;
