@@ -137,6 +137,12 @@ def _arg(fn, name, t, dtypes, count, dev, optional=False):
     raise ValueError(f"{fn}: {name} is on {t.device}, not on the current GPU")
 
 
+def _rows(sh) -> int:
+    """Expert-major rows that a call reads or writes: an empty batch has none,
+    whatever its fixed regions would hold (its arrays may be None)."""
+    return moe_recv_rows(sh) if sh.T else 0
+
+
 def _device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -2   # -1 is the CPU's number
 
@@ -260,7 +266,7 @@ def moe_rmsnorm_quant(sh, x, residual, gamma, eps, res_out, y, y_q, y_s, stream=
 
 def moe_grouped_gemm(sh, x_q, x_s, w_q, w_s, exp_off, K, F, y, stream=None):
     f, dev = "moe_grouped_gemm", _device()
-    rows, kb = moe_recv_rows(sh), K // 128
+    rows, kb = _rows(sh), K // 128
     E = sh.E if sh.T else 0
     _check(f, lib.moe_grouped_gemm(
         ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K, dev), _arg(f, "x_s", x_s, _F32, rows * kb, dev),
@@ -271,7 +277,7 @@ def moe_grouped_gemm(sh, x_q, x_s, w_q, w_s, exp_off, K, F, y, stream=None):
 
 def moe_grouped_gemm_swiglu(sh, x_q, x_s, w13_q, w13_s, exp_off, K, I, a_q, a_s, stream=None):  # noqa: E741
     f, dev = "moe_grouped_gemm_swiglu", _device()
-    rows, kb, ib = moe_recv_rows(sh), K // 128, I // 128
+    rows, kb, ib = _rows(sh), K // 128, I // 128
     E = sh.E if sh.T else 0
     _check(f, lib.moe_grouped_gemm_swiglu(
         ctypes.byref(sh), _arg(f, "x_q", x_q, _F8, rows * K, dev), _arg(f, "x_s", x_s, _F32, rows * kb, dev),
@@ -302,7 +308,7 @@ def moe_layer_ll(sh, tokens, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, I, out,
 
 def moe_ffn_up(sh, x, w13, exp_off, K, I, a, h_q, h_s, stream=None):  # noqa: E741
     f, dev = "moe_ffn_up", _device()
-    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    rows, E = _rows(sh), sh.E if sh.T else 0
     _check(f, lib.moe_ffn_up(
         ctypes.byref(sh), _arg(f, "x", x, _BF16, rows * K, dev), _arg(f, "w13", w13, _BF16, E * 2 * I * K, dev),
         _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, I, _arg(f, "a", a, _BF16, rows * I, dev),
@@ -312,7 +318,7 @@ def moe_ffn_up(sh, x, w13, exp_off, K, I, a, h_q, h_s, stream=None):  # noqa: E7
 
 def moe_grouped_gemm_bf16(sh, x, w, exp_off, K, F, w_t, y, stream=None):
     f, dev = "moe_grouped_gemm_bf16", _device()
-    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    rows, E = _rows(sh), sh.E if sh.T else 0
     _check(f, lib.moe_grouped_gemm_bf16(
         ctypes.byref(sh), _arg(f, "x", x, _BF16, rows * K, dev), _arg(f, "w", w, _BF16, E * F * K, dev),
         _arg(f, "exp_off", exp_off, _I32, sh.N + E if E else 0, dev), K, F, bool(w_t),
@@ -321,7 +327,7 @@ def moe_grouped_gemm_bf16(sh, x, w, exp_off, K, F, w_t, y, stream=None):
 
 def moe_ffn_up_grad(sh, dy, w2, h_q, h_s, exp_off, K, I, dh, a, stream=None):  # noqa: E741
     f, dev = "moe_ffn_up_grad", _device()
-    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    rows, E = _rows(sh), sh.E if sh.T else 0
     _check(f, lib.moe_ffn_up_grad(
         ctypes.byref(sh), _arg(f, "dy", dy, _BF16, rows * K, dev), _arg(f, "w2", w2, _BF16, E * K * I, dev),
         _arg(f, "h_q", h_q, _F8, rows * 2 * I, dev), _arg(f, "h_s", h_s, _F32, rows * (2 * I // 128), dev),
@@ -333,7 +339,7 @@ def moe_ffn_up_grad(sh, dy, w2, h_q, h_s, exp_off, K, I, dh, a, stream=None):  #
 def moe_grouped_wgrad(sh, d, x, exp_off, F, K, dw, add=False, stream=None):
     """dw's type, bfloat16 or float32, says which of the two is written."""
     f, dev = "moe_grouped_wgrad", _device()
-    rows, E = moe_recv_rows(sh), sh.E if sh.T else 0
+    rows, E = _rows(sh), sh.E if sh.T else 0
     out = _arg(f, "dw", dw, _BF16 + _F32, sh.E * F * K, dev)
     _check(f, lib.moe_grouped_wgrad(
         ctypes.byref(sh), _arg(f, "d", d, _BF16, rows * F, dev), _arg(f, "x", x, _BF16, rows * K, dev),
@@ -344,7 +350,7 @@ def moe_grouped_wgrad(sh, d, x, exp_off, F, K, dw, add=False, stream=None):
 
 def moe_combine_grad(sh, dout, y_em, topk_idx, send_pos, topk_w, row_src, ws, dy_em, dtopk_w, stream=None):
     f, dev = "moe_combine_grad", _device()
-    n, rows = sh.N * sh.T, moe_recv_rows(sh) if sh.T else 0
+    n, rows = sh.N * sh.T, _rows(sh)
     _check(f, lib.moe_combine_grad(
         ctypes.byref(sh), _arg(f, "dout", dout, _BF16, n * sh.H, dev),
         _arg(f, "y_em", y_em, _BF16, rows * sh.H, dev, True), _arg(f, "topk_idx", topk_idx, _I32, n * sh.k, dev),

@@ -27,3 +27,13 @@ def test_wgrad_no_tokens(region_rows, dtype):
         assert (dw == 1).all()
         moe.moe_grouped_wgrad(sh, d, x, None, F, K, dw)
         assert (dw == 0).all()
+
+
+def test_wgrad_no_tokens_no_arrays():
+    """The same with no arrays of rows at all."""
+    sh = moe.shape(2, 0, 256, 4, 2, 50)
+    dw = torch.ones((4, 64, 128), device="cuda")
+    moe.moe_grouped_wgrad(sh, None, None, None, 64, 128, dw, add=True)
+    assert (dw == 1).all()
+    moe.moe_grouped_wgrad(sh, None, None, None, 64, 128, dw)
+    assert (dw == 0).all()
