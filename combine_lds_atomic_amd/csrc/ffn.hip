@@ -107,8 +107,13 @@ struct Reader {
   }
 };
 
-// 1 / (1 + exp(-g)); the reciprocal instruction is off by at most one unit in the last place.
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+// 4 / (1 + exp(-g)), with the reciprocal instruction: off by at most one unit in
+// the last place.  That instruction gives 0 where the quotient is subnormal,
+// which 1 / (1 + exp(-g)) is for g from -87.3 down to -88.7, where exp(-g) leaves
+// float32; a quarter of the sum has a normal one, and scaling by 4 is exact.
+__device__ __forceinline__ float sigmoid4(float g) {
+  return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0.25f, 0.25f));
+}
 
 // One workgroup forms BM left features x up to BN right rows of one expert:
 // WM x WN waves of MT x NT matrix tiles of 16 x 16, so a lane holds four
@@ -141,7 +146,6 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
   constexpr int NW = WM * WN, THREADS = NW * kWave;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LL = BM * kStepBytes / 1024 / NW, LR = BN * kStepBytes / 1024 / NW;   // loads of a wave and stage
-  constexpr int LPS = LL + LR;
   static_assert(LL * NW * 1024 == BM * kStepBytes && LR * NW * 1024 == BN * kStepBytes, "loads split evenly");
   static_assert(MT % (EPI == Epi::kUp ? 4 : 2) == 0, "the epilogue takes tiles in pairs");
   static_assert(EPI != Epi::kUp || (BM == 2 * kScaleBlock && LL % 2 == 0), "a gate and an up half of one scale block");
@@ -474,9 +478,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = fp8_value(gq[p][i / 4], i & 3) * gs[p], u = fp8_value(uq[p][i / 4], i & 3) * us[p];
-          const float s = sigmoid(g), y = g * s;
+          const float q = sigmoid4(g), s = 0.25f * q, y = 0.25f * g * q;
           du[i] = da[i] * y;
-          dg[i] = da[i] * u * (s * (1.0f + g * (1.0f - s)));
+          dg[i] = da[i] * u * (q * (0.25f + 0.25f * g * (1.0f - s)));
           av[i] = y * u;
         }
         if (tok < n && f < A.F) {
@@ -503,7 +507,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
         pair(m + MT / 2, j, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = g[i] * sigmoid(g[i]) * u[i];
+          v[i] = 0.25f * g[i] * sigmoid4(g[i]) * u[i];
           mg = max(mg, abs_bits(g[i]));
           mu = max(mu, abs_bits(u[i]));
           // kept in the new order

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import combine_lds_atomic_amd as moe
+import expert_ref as X
+import training_ref as R
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,38 @@ def test_wgrad_no_tokens_no_arrays():
     assert (dw == 1).all()
     moe.moe_grouped_wgrad(sh, None, None, None, 64, 128, dw)
     assert (dw == 0).all()
+
+
+def test_gates_whose_sigmoid_is_subnormal():
+    """silu and its slope where 1 / (1 + exp(-g)) is below float32's normal range
+    but exp(-g) is still in it: u of 1e30 brings the products back into bf16's."""
+    log("subnormal sigmoids")
+    H = I = 128  # noqa: E741
+    parts = torch.tensor([[-80.0, 0.0], [-87.0, -0.25], [-87.0, -0.5], [-88.0, 0.0], [-88.5, 0.0], [-88.5, -0.1875]])
+    n = len(parts)
+    sh, eo = moe.shape(1, n, 128, 1, 1), torch.tensor([[0, n]], dtype=torch.int32, device="cuda")
+    x = torch.zeros((n, H), dtype=BF, device="cuda")
+    x[:, :2], x[:, 2] = parts.cuda().to(BF), 1.0
+    w13, w2 = (torch.zeros(s, dtype=BF, device="cuda") for s in ((1, 2 * I, H), (1, H, I)))
+    w13[0, :I, :2], w13[0, I:, 2], w2[0, 0] = 1.0, 1e30, 1.0
+    dy = torch.zeros((n, H), dtype=BF, device="cuda")
+    dy[:, 0] = 1.0
+    a, dh, a2 = (torch.empty((n, m), dtype=BF, device="cuda") for m in (I, 2 * I, I))
+    q, s = torch.empty((n, 2 * I), dtype=torch.uint8, device="cuda"), torch.empty((n, 2), device="cuda")
+    moe.moe_ffn_up(sh, x, w13, eo, H, I, a, q, s)
+    moe.moe_ffn_up_grad(sh, dy, w2, q, s, eo, H, I, dh, a2)
+
+    def close(got, want, g):
+        # the exponential's argument rounded twice (|g| 2^-23 of the result each way), some
+        # twenty roundings, then bf16's half step; nothing cancels for g this far from 0
+        lim = want.abs() * (X.BF16_HALF + (2 * g.abs() + 24) * R.U)
+        bad = bool(((got.double() - want).abs() > lim).any())
+        assert not bad, (got[:, 0].tolist(), want[:, 0].tolist())
+    g = (x[:, :1].double() + x[:, 1:2].double()).expand(n, I)
+    close(a, g * torch.sigmoid(g) * w13[0, I, 2].double(), g)
+    h = X.values(q, s)
+    g, u = h[:, :I], h[:, I:]
+    t = torch.sigmoid(g)
+    close(a2, g * t * u, g)
+    close(dh[:, :I], u * t * (1 + g * (1 - t)), g)
+    close(dh[:, I:], g * t, g)
