@@ -193,9 +193,12 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 //
 // r is linear in 1 / rms(x), so one reduction of seven sums gives both roots,
 // the part of t along r and dgate, where a reduction after each of them would
-// be three.  The sum of r^2 comes out of its three parts; where the residual
-// and the block's term cancel to less than an eighth of those, it is formed
-// from r itself in a second reduction.
+// be three.  The sum of r^2 comes out of its three parts.  That asks two things
+// of a row: the residual and the block's term do not cancel to less than an
+// eighth of the parts, and the squares of x * gamma_post, which the formula has
+// only after the division by rms(x), neither leave float32 nor lose digits that
+// count beside eps.  Where they do, the five sums that the roots are followed by
+// are formed from r and x / rms(x) themselves in a second reduction.
 //
 // Bound by HBM and, nearly as much, by its 350 vector instructions a wave and
 // row: 1001 to 1097 us for 65536 rows of 7168 (12 H bytes a row, 5.1 to 5.6
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 // 2.1 since, some registers still go to scratch.
 template <int U, bool KEEP>
 __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
-  __shared__ float part[2][kMaxWaves][8], one[kMaxWaves];
+  __shared__ float part[2][kMaxWaves][8], again[kMaxWaves][8];
   const int threads = blockDim.x, units = A.H / 8;
   const v4u zero = {0, 0, 0, 0};
   const float h = 1.0f / (float)A.H;
@@ -304,27 +307,48 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
     row_sum8(m, part[turn]);
     const float i1 = rsqrtf(m[0] * h + A.eps), b = gate * i1;
     const float apart = A.alpha * A.alpha * m[2] + b * b * m[1];
-    float rr = apart + 2.0f * A.alpha * b * m[3];
-    if (!(rr >= 0.125f * apart)) {   // the residual and the block nearly cancel: the sum of r itself
-      float v = 0.0f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+    float rr = apart + 2.0f * A.alpha * b * m[3];                  // r r
+    float tr = A.alpha * m[4] + b * m[5];                          // t r
+    float unit = i1, rx = A.alpha * m[3] + b * m[1];               // unit: what the sums with x gp still lack
+    // 2^-149 is the least step of a square, 2^-24 what counts beside eps
+    const bool apart_ok = apart < __builtin_inff() && b * b * 0x1p-125f < A.eps;
+    if (__builtin_expect(!(rr >= 0.125f * apart && apart_ok), 0)) {
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {   // not unrolled: what the rest keeps in registers stays there
         bring(u);
-        float x[8], r[8], g[8];
-        unpack8(q.x[KEEP ? u : 0], x);
-        unpack8(q.r[KEEP ? u : 0], r);
-        unpack8(gp[KEEP ? u : 0], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float w = A.alpha * r[i] + b * (x[i] * g[i]);
-          v = __builtin_fmaf(w, w, v);
+        for (int half = 0; half < 2; ++half) {
+          float x[4], r[4], g[4], n[4], t[4], d[4];
+          unpack4(q.x[KEEP ? u : 0], half, x);
+          unpack4(q.r[KEEP ? u : 0], half, r);
+          unpack4(gp[KEEP ? u : 0], half, g);
+          unpack4(gn[KEEP ? u : 0], half, n);
+          unpack4(q.t[KEEP ? u : 0], half, t);
+          unpack4(q.d[KEEP ? u : 0], half, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float xg = x[i] * i1 * g[i], w = A.alpha * r[i] + gate * xg, tn = t[i] * n[i];
+            v[0] = __builtin_fmaf(w, w, v[0]);
+            v[1] = __builtin_fmaf(tn, w, v[1]);
+            v[2] = __builtin_fmaf(w, xg, v[2]);
+            v[3] = __builtin_fmaf(tn, xg, v[3]);
+            v[4] = __builtin_fmaf(d[i], xg, v[4]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      rr = row_sum<false>(v, one);
+      row_sum8(v, again);
+      rr = v[0];
+      tr = v[1];
+      rx = v[2];
+      m[5] = v[3];
+      m[6] = v[4];
+      unit = 1.0f;
     }
     const float i2 = rsqrtf(rr * h + A.eps);
-    const float along = (A.alpha * m[4] + b * m[5]) * h * i2 * i2;
-    const float dg = i1 * (m[6] + i2 * (m[5] - along * (A.alpha * m[3] + b * m[1])));
+    const float along = tr * h * i2 * i2;
+    const float dg = unit * (m[6] + i2 * (m[5] - along * rx));
     if (threadIdx.x == 0 && A.dgate) A.dgate[row] = dg;
     const float k0 = i1 * i1 * gate * dg * h, k1 = i2 * along;
 #pragma unroll

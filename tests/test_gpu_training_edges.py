@@ -5,6 +5,7 @@ import torch
 
 import combine_lds_atomic_amd as moe
 import expert_ref as X
+import test_gpu_training as base
 import training_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +75,22 @@ def test_gates_whose_sigmoid_is_subnormal():
     close(a2, g * t * u, g)
     close(dh[:, :I], u * t * (1 + g * (1 - t)), g)
     close(dh[:, I:], g * t, g)
+
+
+# ------------------------------------------------------------------ norm gradients
+
+@pytest.mark.parametrize("x_scale,g_scale,eps", [
+    (1e15, 1e4, 1e-5),        # squares of x * gamma_post leave float32, those of x and of the outputs do not
+    (1e10, 1e10, 1e-5),
+    (1e-15, 1e-10, 1e-30),    # and those that vanish, with an eps that they count beside
+])
+@pytest.mark.parametrize("H", [1024, 8320, 20480])
+def test_block_norm_grad_number_range(H, x_scale, g_scale, eps):
+    log(f"block norm H={H} x of {x_scale} gamma of {g_scale}")
+    g = base.gen(H)
+    sh, N, T = moe.shape(1, 3, H, 1, 1), 1, 3
+    x, res, dy, dr = (base.normal((N, T, H), g, s) for s in (x_scale, 4 * g_scale, 1.0, 1 / g_scale))
+    gp, gn = (((1 + 0.2 * torch.randn(H, generator=g, device="cuda")) * s).to(BF) for s in (g_scale, 1.0))
+    gate = torch.randn((N, T), generator=g, device="cuda")
+    base.check_norm(sh, x, res, gp, gate, 0.75, gn, eps)
+    base.check_norm_grad(sh, dy, dr, x, res, gp, gate, 0.75, gn, eps)
