@@ -94,3 +94,79 @@ def test_block_norm_grad_number_range(H, x_scale, g_scale, eps):
     gate = torch.randn((N, T), generator=g, device="cuda")
     base.check_norm(sh, x, res, gp, gate, 0.75, gn, eps)
     base.check_norm_grad(sh, dy, dr, x, res, gp, gate, 0.75, gn, eps)
+
+
+@pytest.mark.parametrize("N,T,H", [(2, 300, 8320), (1, 700, 16384), (1, 1300, 20480), (1, 600, 32768)])
+def test_block_norm_many_wide_rows_and_in_place(N, T, H):
+    """More than one row a workgroup, and outputs over inputs, in the forms that
+    read a row again."""
+    base.test_block_norm_many_rows_and_in_place(N, T, H)
+
+
+@pytest.mark.parametrize("N,T,H", [(1, 300, 2048), (2, 300, 8320), (1, 9, 16384), (1, 300, 32768)])
+def test_block_norm_grad_where_wide_rows_cancel(N, T, H):
+    """Every second row's residual is minus the block's term but for a rounding and a
+    few columns, so that both reductions alternate in a workgroup."""
+    log(f"block norm cancelling N={N} T={T} H={H}")
+    sh, x, res, gp, gate, gn, dy, dr = base.norm_case(N, T, H, H)
+    x = base.normal((N, T, H), base.gen(4))
+    n1 = x.double() / torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + 1e-5) * gp.double()
+    near = (-gate.double()[..., None] * n1).to(BF)
+    near[..., :8] = 0
+    res[:, ::2] = near[:, ::2]
+    base.check_norm(sh, x, res, gp, gate, 1.0, gn)
+    got = base.check_norm_grad(sh, dy, dr, x, res, gp, gate, 1.0, gn)
+    ws = torch.empty(moe.moe_block_norm_grad_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    dgate, dgp, dgn = torch.empty_like(gate), torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    moe.moe_block_norm_grad(sh, dy, dr, x, res, gp, gate, 1.0, gn, 1e-5, x, res, dgate, dgp, dgn, ws)
+    for n, t in (("dx", x), ("dresidual", res), ("dgate", dgate), ("dgamma_post", dgp), ("dgamma_next", dgn)):
+        assert torch.equal(t, got[n]), n
+
+
+# ------------------------------------------------------------------ long sums
+
+def chain_limit(K):
+    """Relative to the norm of many sums of K products: an instruction takes 32
+    products, in up to four groups that join the running sum one after the
+    other.  Each join is off by half a float32 step at most, of a partial sum
+    that is no larger in norm than the whole; independent, they add up as the
+    root of their number.  Four more roundings for what follows the sum."""
+    return R.U * ((4 * K / 32 / 3) ** 0.5 + 4)
+
+
+@pytest.mark.parametrize("kind", ["any sign", "positive"])
+def test_weight_gradients_of_many_rows(kind):
+    """float32 gradients of an expert with tens of thousands of rows: the error
+    grows as the root of the rows, not with their number."""
+    log(f"wgrad of many rows, {kind}")
+    g, counts, F, K = base.gen(8), [65536, 100, 30001], 272, 400
+    rows = sum(counts)
+    sh, eo = moe.shape(1, rows, 128, 3, 1), base.make_groups(1, 3, counts)
+    d, x = base.normal((rows, F), g), base.normal((rows, K), g)
+    if kind == "positive":
+        d, x = d.abs(), x.abs()
+    dw = torch.empty((3, F, K), device="cuda")
+    moe.moe_grouped_wgrad(sh, d, x, eo, F, K, dw)
+    for e, a, n in X.group_rows(eo, rows, 0):
+        want = d[a:a + n].double().T @ x[a:a + n].double()
+        rel = ((dw[e].double() - want).norm() / want.norm()).item()
+        log(f"  {n} rows: {rel:.2e} of the norm")
+        assert rel <= chain_limit(n)
+
+
+@pytest.mark.parametrize("K", [7168, 32768])
+def test_checkpoint_scales_of_the_large_tile(K):
+    """h_s of the tile that has no registers to join its sums in parts."""
+    log(f"checkpoint scales K={K}")
+    g, rows, I = base.gen(K), 4096, 4096  # noqa: E741
+    sh, eo = moe.shape(1, rows, 128, 1, 1), base.make_groups(1, 1, [rows])
+    x, w13 = base.normal((rows, K), g), base.normal((1, 2 * I, K), g, K ** -0.5)
+    a = torch.empty((rows, I), dtype=BF, device="cuda")
+    q, s = torch.empty((rows, 2 * I), dtype=torch.uint8, device="cuda"), torch.empty((rows, 2 * I // 128), device="cuda")
+    moe.moe_ffn_up(sh, x, w13, eo, K, I, a, q, s)
+    some = torch.cat((torch.arange(100), torch.arange(rows - 100, rows))).cuda()
+    h = x[some].double() @ w13[0].double().T
+    want = h.view(len(some), -1, 128).abs().amax(-1) / 448
+    rel = ((s[some].double() - want).norm() / want.norm()).item()
+    log(f"  {rel:.2e} of the norm")
+    assert rel <= chain_limit(K)
