@@ -197,17 +197,19 @@ __global__ __launch_bounds__(WAVE ? 4 * kWave : kMaxThreads) void k_block_norm(B
 // of a row: the residual and the block's term do not cancel to less than an
 // eighth of the parts, and the squares of x * gamma_post, which the formula has
 // only after the division by rms(x), neither leave float32 nor lose digits that
-// count beside eps.  Where they do, the five sums that the roots are followed by
-// are formed from r and x / rms(x) themselves in a second reduction.
+// count beside eps.  For a row that fails either, the five sums that follow the
+// first root are formed from r and x / rms(x) themselves in a second reduction.
 //
 // Bound by HBM and, nearly as much, by its 350 vector instructions a wave and
-// row: 1001 to 1097 us for 65536 rows of 7168 (12 H bytes a row, 5.1 to 5.6
+// row: 991 to 1097 us for 65536 rows of 7168 (12 H bytes a row, 5.1 to 5.7
 // TB/s).  One unit a thread leaves registers for the next row's loads; two
 // units took 1146, three reductions a row 1184, and 2 workgroups a compute
 // unit without loads ahead 2.4 ms, since registers went to scratch.  Rows above 8192
-// are read twice (958 us at 32768 rows of 8320, 1270 with all of it in registers
-// and scratch); at H = 32768, with 1.3 TB/s before one of the sums went to LDS and
-// 2.1 since, some registers still go to scratch.
+// are read twice: 869 to 925 us at 32768 rows of 8320 (484 at a copy's rate with one
+// reading), 1270 with all of it in registers and scratch.  Both of their forms
+// still send some registers to scratch, 10 with two units a thread and 80 with
+// four (8192 rows of 32768: 1.51 to 1.56 ms, 2.1 TB/s; 1.3 before one of the
+// sums went to LDS).
 template <int U, bool KEEP>
 __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
   __shared__ float part[2][kMaxWaves][8], again[kMaxWaves][8];
@@ -309,7 +311,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
     const float apart = A.alpha * A.alpha * m[2] + b * b * m[1];
     float rr = apart + 2.0f * A.alpha * b * m[3];                  // r r
     float tr = A.alpha * m[4] + b * m[5];                          // t r
-    float unit = i1, rx = A.alpha * m[3] + b * m[1];               // unit: what the sums with x gp still lack
+    float rx = A.alpha * m[3] + b * m[1];                          // r x gp
+    float lack = i1;                                               // what the sums with x gp lack of x / rms(x)
     // 2^-149 is the least step of a square, 2^-24 what counts beside eps
     const bool apart_ok = apart < __builtin_inff() && b * b * 0x1p-125f < A.eps;
     if (__builtin_expect(!(rr >= 0.125f * apart && apart_ok), 0)) {
@@ -344,11 +347,11 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs A) {
       rx = v[2];
       m[5] = v[3];
       m[6] = v[4];
-      unit = 1.0f;
+      lack = 1.0f;
     }
     const float i2 = rsqrtf(rr * h + A.eps);
     const float along = tr * h * i2 * i2;
-    const float dg = unit * (m[6] + i2 * (m[5] - along * rx));
+    const float dg = lack * (m[6] + i2 * (m[5] - along * rx));
     if (threadIdx.x == 0 && A.dgate) A.dgate[row] = dg;
     const float k0 = i1 * i1 * gate * dg * h, k1 = i2 * along;
 #pragma unroll
@@ -450,8 +453,9 @@ inline int grad_threads(int H) {
 }
 
 // Workgroups of the gradient's first kernel: what 256 compute units hold at
-// once, but at least four rows each beyond 256 rows, since the sums that a
-// workgroup leaves are as many bytes as one row and a third.
+// once, but not above the larger of 256 and a quarter of the rows (so from 1024
+// rows on at least four rows each, below that one to four), since the sums that
+// a workgroup leaves, written and read, are as many bytes as one row and a third.
 inline int64_t grad_groups(const Dims& D) {
   const int64_t rows = (int64_t)D.N * D.T, most = 256 * (1024 / grad_threads(D.H));
   if (rows <= 256) return rows;

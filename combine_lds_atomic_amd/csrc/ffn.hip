@@ -11,6 +11,12 @@
 // All of them are one kernel: a left operand (features, the matrix
 // instruction's rows) times a right one (tokens; for wgrad the other side's
 // features), with float32 sums, each output rounded once.
+//
+// a and dh are rounded to bf16 where a call ends, because they are operands of
+// the next call's matrix instructions: keeping them in 32 bits would take two
+// bf16 parts, so twice the products.  What follows them is then two roundings
+// away from the formula: y, dx and the weight gradients are off by 0.00235 of
+// their norm, 0.00166 with one rounding (E = 16, 64 rows each, H = I = 2048).
 #include <type_traits>
 
 #include "gemm_dev.h"
@@ -111,6 +117,9 @@ struct Reader {
 // the last place.  That instruction gives 0 where the quotient is subnormal,
 // which 1 / (1 + exp(-g)) is for g from -87.3 down to -88.7, where exp(-g) leaves
 // float32; a quarter of the sum has a normal one, and scaling by 4 is exact.
+// With a division instead (correctly rounded), up and down of 2048 rows for each
+// of 32 experts took 4.97 to 5.02 ms against 4.94 to 4.95, all gradients 10.03
+// against 9.99.
 __device__ __forceinline__ float sigmoid4(float g) {
   return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0.25f, 0.25f));
 }
@@ -124,7 +133,8 @@ __device__ __forceinline__ float sigmoid4(float g) {
 // 2048; ranges are over machines and runs): up 3.25 to 3.43 ms (1.12 to 1.18
 // PFLOP/s), down 1.65 to 1.73, the transposed product 3.11 to 3.24 (1.19 to 1.24), up
 // gradient 1.87 to 1.95 (0.99 to 1.03), weight gradients 3.21 to 3.33 and 1.55 to
-// 1.60 (1.16 to 1.24); large library products of the three layouts reach 1.60 (rows
+// 1.61 (1.16 to 1.24; added 3.57 and 1.77, in float32 3.50 and 1.74, added there
+// 4.28 and 2.11); large library products of the three layouts reach 1.60 (rows
 // x rows), 1.38 and 1.18.  The matrix pipes are busy 51% to 64% of the cycles
 // at a clock that falls to 1.77 to 1.9 GHz; LDS reads have no bank conflicts.
 // Timing copies: with loads that stay on two steps (so in L2) 3.00 ms for up and 3.02
@@ -302,6 +312,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_ffn_product(ProductArgs A) {
     // in them (K = 2048: 2.5e-7 of a value against a library product's 1.1e-7).
     // So the sums of 128 columns (narrow tile, bound by the weights' stream) or
     // 512 (middle tile) join a total; the large tile has no registers for one.
+    // Of the scales' norm at K = 7168: middle tile 8.5e-8, large tile 4.7e-7, a
+    // float32 product of the library 8.9e-7; at K = 32768 large tile 9.9e-7, library
+    // 2.3e-6.  Float32 weight gradients have no total either: their error grows as the
+    // root of the rows, 1.6e-6 of the norm at 65536 (library 1.9e-6).
     constexpr int kJoin = EPI != Epi::kUp ? 0 : BN <= 32 ? 2 : BN <= 128 ? 8 : 0;   // steps
     v4f total[kJoin ? MT : 1][kJoin && NL > 0 ? NL : 1] = {};
     v8bf a[2][MT], b[2][NL > 0 ? NL : 1];
